@@ -41,7 +41,8 @@ LIB = os.path.join(PKG, "libpq1.so")
 BENCH_LIB = os.path.join(PKG, "libpq1_bench.so")
 ARCH = "gfx950"
 
-SOURCES = ["api.hip", "rotate.hip", "gemv.hip", "gemv_packed.hip", "gemm.hip", "gemm_skinny.hip"]
+SOURCES = ["api.hip", "rotate.hip", "gemv.hip", "gemv_packed.hip", "gemm.hip", "gemm_skinny.hip",
+           "api_attention.hip", "rope.hip", "paged_attention.hip"]
 BENCH_SOURCES = ["bench_kernels.hip"]
 
 # gemm_skinny.hip: MFMA results stay in ordinary VGPRs (the per-group fold

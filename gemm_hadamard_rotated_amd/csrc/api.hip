@@ -10,6 +10,7 @@
 #include <mutex>
 #include <unordered_map>
 
+#include "api_checks.h"
 #include "pq1.h"
 #include "pq1_internal.h"
 
@@ -29,12 +30,10 @@ std::atomic<uint32_t> g_test_flags{0};
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = (int64_t{1} << 31) - 1;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + bn && b0 < a0 + an;
-}
+using pq1::aligned16;
+using pq1::check_device;
+using pq1::launched;
+using pq1::overlaps;
 
 // Per-device "is this a gfx950" cache (and its compute-unit count); checked
 // once per device.
@@ -43,7 +42,40 @@ int g_dev_state[kMaxDevices];  // 0 unknown, 1 ok, 2 wrong architecture
 int g_dev_cus[kMaxDevices];
 std::mutex g_dev_mu;
 
-pq1_status check_device(int* cus = nullptr) {
+pq1_status check_perm(const pq1_perm* perm, int64_t K, pq1::Perm* out) {
+  *out = pq1::Perm{};
+  if (perm == nullptr || perm->rep <= 1) return PQ1_OK;
+  if (perm->hd < 1 || perm->nk < 1) return PQ1_ERR_PERM;
+  if (perm->hd % 4 != 0) return PQ1_ERR_PERM;
+  if (static_cast<int64_t>(perm->hd) * perm->nk * perm->rep != K) return PQ1_ERR_PERM;
+  out->hd = perm->hd;
+  out->nk = perm->nk;
+  out->rep = perm->rep;
+  out->on = true;
+  return PQ1_OK;
+}
+
+pq1_status check_weights(const uint32_t* w_bits, const float* scales, int64_t N, int64_t K) {
+  if (w_bits == nullptr || scales == nullptr) return PQ1_ERR_NULL;
+  if (N < 1 || K < 128 || K % 128 != 0) return PQ1_ERR_SHAPE;
+  if (N > kMaxDim || K > kMaxDim || N * (K / 32) > kMaxElems) return PQ1_ERR_SHAPE;
+  if (!aligned16(w_bits) || !aligned16(scales)) return PQ1_ERR_ALIGN;
+  return PQ1_OK;
+}
+
+pq1_status check_workspace(const pq1::GemvPlan& plan, void* workspace, size_t ws_bytes) {
+  if (plan.nkt <= 1) return PQ1_OK;  // single K-tile: workspace unused
+  if (workspace == nullptr) return PQ1_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PQ1_ERR_ALIGN;
+  if (ws_bytes < plan.workspace_bytes()) return PQ1_ERR_ARG;
+  return PQ1_OK;
+}
+
+}  // namespace
+
+namespace pq1 {
+
+pq1_status check_device(int* cus) {
   int dev = -1;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -80,36 +112,7 @@ pq1_status launched(hipError_t e) {
   return PQ1_OK;
 }
 
-pq1_status check_perm(const pq1_perm* perm, int64_t K, pq1::Perm* out) {
-  *out = pq1::Perm{};
-  if (perm == nullptr || perm->rep <= 1) return PQ1_OK;
-  if (perm->hd < 1 || perm->nk < 1) return PQ1_ERR_PERM;
-  if (perm->hd % 4 != 0) return PQ1_ERR_PERM;
-  if (static_cast<int64_t>(perm->hd) * perm->nk * perm->rep != K) return PQ1_ERR_PERM;
-  out->hd = perm->hd;
-  out->nk = perm->nk;
-  out->rep = perm->rep;
-  out->on = true;
-  return PQ1_OK;
-}
-
-pq1_status check_weights(const uint32_t* w_bits, const float* scales, int64_t N, int64_t K) {
-  if (w_bits == nullptr || scales == nullptr) return PQ1_ERR_NULL;
-  if (N < 1 || K < 128 || K % 128 != 0) return PQ1_ERR_SHAPE;
-  if (N > kMaxDim || K > kMaxDim || N * (K / 32) > kMaxElems) return PQ1_ERR_SHAPE;
-  if (!aligned16(w_bits) || !aligned16(scales)) return PQ1_ERR_ALIGN;
-  return PQ1_OK;
-}
-
-pq1_status check_workspace(const pq1::GemvPlan& plan, void* workspace, size_t ws_bytes) {
-  if (plan.nkt <= 1) return PQ1_OK;  // single K-tile: workspace unused
-  if (workspace == nullptr) return PQ1_ERR_NULL;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PQ1_ERR_ALIGN;
-  if (ws_bytes < plan.workspace_bytes()) return PQ1_ERR_ARG;
-  return PQ1_OK;
-}
-
-}  // namespace
+}  // namespace pq1
 
 uint32_t pq1::test_flags() { return g_test_flags.load(std::memory_order_relaxed); }
 

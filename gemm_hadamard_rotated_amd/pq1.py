@@ -8,6 +8,7 @@ if the library is missing or the tensors are not on a GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional, Sequence
@@ -18,7 +19,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("PQ1_LIBRARY") or os.path.join(_HERE, "libpq1.so")
 
 PQ1_OK = 0
-PQ1_F32, PQ1_BF16, PQ1_BF16_GEMM = 0, 1, 2
+PQ1_F32, PQ1_BF16, PQ1_BF16_GEMM, PQ1_F16 = 0, 1, 2, 3
+PQ1_ROPE_HALVES, PQ1_ROPE_ADJACENT = 0, 1
 PQ1_X_ROW_MAJOR, PQ1_X_GEMM_ORDER = 0, 1
 PQ1_GEMV_AUTO, PQ1_GEMV_LUT, PQ1_GEMV_EXPAND = 0, 1, 2
 PQ1_GEMV_COUNTER_BYTES = 262144  # split-K bookkeeping at the start of a GEMV workspace
@@ -37,7 +39,8 @@ EXPORTS = ("pq1_rotate", "pq1_gemv_workspace_bytes", "pq1_gemv", "pq1_gemv_ex",
            "pq1_pack_weights_ex", "pq1_embed", "pq1_gemv_packed", "pq1_rotate_gemv_packed",
            "pq1_gemv_packed_ex", "pq1_rotate_gemv_packed_ex", "pq1_gemm", "pq1_gemm_ex",
            "pq1_status_str", "pq1_abi_version", "pq1_last_hip_error", "pq1_set_test_flags",
-           "pq1_rotate_gemv_packed_noalloc")
+           "pq1_rotate_gemv_packed_noalloc", "pq1_rope", "pq1_kv_append",
+           "pq1_paged_attention", "pq1_paged_attention_workspace_bytes")
 
 
 class Pq1Error(RuntimeError):
@@ -48,6 +51,23 @@ class Pq1Error(RuntimeError):
 
 class Pq1Perm(ctypes.Structure):
     _fields_ = [("hd", ctypes.c_int32), ("nk", ctypes.c_int32), ("rep", ctypes.c_int32)]
+
+
+class Pq1Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Pq1RopeSpec(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("section", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("inverse", ctypes.c_int32)]
+
+
+class Pq1KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("pages", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
 
 
 _lib = None
@@ -66,6 +86,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib = ctypes.CDLL(path)
         P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         PP = ctypes.POINTER(Pq1Perm)
+        PH, PS, PC = (ctypes.POINTER(c) for c in (Pq1Heads, Pq1RopeSpec, Pq1KvCache))
         sig = {
             "pq1_rotate": (I32, [P, P, PP, P, I32, I64, I64, P]),
             "pq1_gemv_workspace_bytes": (SZ, [I64, I64]),
@@ -87,6 +108,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "pq1_gemm_ex": (I32, [P, P, P, P, I64, I64, I64, I32, P]),
             "pq1_set_test_flags": (ctypes.c_uint32, [ctypes.c_uint32]),
             "pq1_rotate_gemv_packed_noalloc": (I32, [P, P, PP, P, P, I32, P, I64, I64, P]),
+            "pq1_rope": (I32, [PH, PH, P, P, PS, I64, I32, I32, P]),
+            "pq1_kv_append": (I32, [PH, PH, P, PH, PH, I32, P, P, PS, PC, I64, P]),
+            "pq1_paged_attention": (I32, [PH, PH, PC, P, I64, P, P, I64, I64, I32, I64, I64,
+                                          ctypes.c_float, I32, I32, P, SZ, P]),
+            "pq1_paged_attention_workspace_bytes": (SZ, [I64, I64, I32, I32, I32, I64, I64]),
             "pq1_status_str": (ctypes.c_char_p, [I32]),
             "pq1_abi_version": (I32, []),
             "pq1_last_hip_error": (I32, []),
@@ -581,7 +607,8 @@ def pq1_rotate_gemv_packed_noalloc(x: torch.Tensor, signs: torch.Tensor, pw: Pac
         _check(lib.pq1_rotate_gemv_packed_noalloc(_ptr(x), _ptr(signs), _perm(perm), _ptr(pw.bits),
                                                   _ptr(pw.scales), _scale_code(pw.scale_dtype),
                                                   _ptr(out), pw.N, x.numel(), _stream(dev)),
-               "pq1_rotate_gemv_packed_noalloc")
+               "pq1_rotate_gemv_packed_noalloc", "pq1_rope", "pq1_kv_append",
+           "pq1_paged_attention", "pq1_paged_attention_workspace_bytes")
     return out
 
 
@@ -633,3 +660,260 @@ def pq1_abi_version() -> int:
 
 def pq1_gemv_workspace_bytes(N: int, K: int) -> int:
     return int(load_library().pq1_gemv_workspace_bytes(int(N), int(K)))
+
+
+# ----------------------------------------------------------------------------
+# Attention layer: rotation by positions, the paged cache, attention over it
+# ----------------------------------------------------------------------------
+_TYPE_CODE = {torch.float32: PQ1_F32, torch.bfloat16: PQ1_BF16, torch.float16: PQ1_F16}
+_FLOATS = tuple(_TYPE_CODE)
+_PAIRINGS = {"halves": PQ1_ROPE_HALVES, "adjacent": PQ1_ROPE_ADJACENT}
+
+
+def _need_heads(t: torch.Tensor, name: str, dtypes, dev=None) -> Pq1Heads:
+    """A [tokens][heads][dim] tensor with contiguous head vectors, as the
+    library's view of it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU (no CPU path exists)")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D, [tokens][heads][dim]")
+    ts, hs, ds = t.stride()
+    if ds != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    # the stride of an axis of length one says nothing
+    if t.shape[0] <= 1:
+        ts = 0
+    if t.shape[1] <= 1:
+        hs = 0
+    return Pq1Heads(t.data_ptr(), _TYPE_CODE[t.dtype], ts, hs)
+
+
+def _need_shape(t: torch.Tensor, name: str, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _launch(dev: torch.device, where: str, fn, *args):
+    """fn(*args, current stream of dev) with dev current."""
+    if torch.cuda.current_device() == dev.index:
+        code = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, _stream(dev))
+    _check(code, where)
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """The [rot / 2] fp64 frequencies base^(-2i / rot), radians per position."""
+    i = torch.arange(int(rot) // 2, dtype=torch.float64, device=device)
+    return torch.exp(i * (-2.0 * math.log(base) / int(rot)))
+
+
+class Rope:
+    """A rotation by positions, made once and used by every call: the first
+    `rot` elements of a head turn, `sections` gives the pairs that each
+    position axis owns (include/pq1.h, pq1_rope_spec).
+
+    freqs  [rot / 2] fp64 on the GPU, radians per position (rope_frequencies,
+           or any scaled variant of them).
+    """
+
+    def __init__(self, rot: int, sections: Optional[Sequence[int]] = None, *,
+                 freqs: torch.Tensor, pairing: str = "halves", interleaved: bool = False):
+        _need(freqs, "freqs", (torch.float64,))
+        rot = int(rot)
+        if rot < 2 or rot % 2 != 0:
+            raise Pq1Error(2, "Rope", f"rot must be even and at least 2, got {rot}")
+        _need_numel(freqs, "freqs", rot // 2)
+        sections = [rot // 2] if sections is None else [int(s) for s in sections]
+        if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != rot // 2:
+            raise Pq1Error(2, "Rope", f"one to four sections of together {rot // 2} pairs, "
+                                      f"got {sections}")
+        if pairing not in _PAIRINGS:
+            raise Pq1Error(8, "Rope", f"unknown pairing {pairing!r} (halves or adjacent)")
+        self.rot, self.sections, self.axes, self.freqs = rot, sections, len(sections), freqs
+        padded = (sections + [0, 0, 0])[:4]
+        self._spec = tuple(
+            Pq1RopeSpec(rot, len(sections), (ctypes.c_int32 * 4)(*padded), int(bool(interleaved)),
+                        _PAIRINGS[pairing], inverse) for inverse in (0, 1))
+
+    def _need_positions(self, positions: torch.Tensor, T: int, dev):
+        _need(positions, "positions", (torch.int32,), dev)
+        _need_numel(positions, "positions", self.axes * T)
+        if positions.dim() != 1 or self.axes != 1:
+            _need_shape(positions, "positions", (self.axes, T))
+        if self.freqs.device != dev:
+            raise ValueError(f"the rotation's freqs are on {self.freqs.device}, expected {dev}")
+
+
+def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
+             out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+             inverse: bool = False) -> torch.Tensor:
+    """x [T][H][D] rotated by positions ([axes][T] int32, or [T] for one axis).
+
+    x may be a slice (contiguous heads); out may be x itself.  inverse=True
+    turns back, which is also the gradient of the forward call."""
+    xv = _need_heads(x, "x", _FLOATS)
+    dev = x.device
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    T, H, D = x.shape
+    rope._need_positions(positions, T, dev)
+    if out is None:
+        dt = x.dtype if out_dtype is None else out_dtype
+        if dt not in _TYPE_CODE:
+            raise TypeError(f"out_dtype must be in {_FLOATS}")
+        out = torch.empty((T, H, D), dtype=dt, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
+    yv = _need_heads(out, "out", _FLOATS, dev)
+    _need_shape(out, "out", (T, H, D))
+    _launch(dev, "pq1_rope", load_library().pq1_rope, xv, yv, _ptr(positions), _ptr(rope.freqs),
+            rope._spec[bool(inverse)], T, H, D)
+    return out
+
+
+class KVCache:
+    """A paged key/value cache over two tensors of the caller's,
+    [pages][heads][page_size][dim], bf16 or f16 (include/pq1.h, pq1_kv_cache)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _need(k, "k", (torch.bfloat16, torch.float16))
+        _need(v, "v", (k.dtype,), k.device)
+        if k.dim() != 4:
+            raise ValueError("k must be 4-D, [pages][heads][page_size][dim]")
+        _need_shape(v, "v", k.shape)
+        self.k, self.v = k, v
+        self.pages, self.heads, self.page_size, self.dim = (int(n) for n in k.shape)
+        self._struct = Pq1KvCache(k.data_ptr(), v.data_ptr(), _TYPE_CODE[k.dtype],
+                                  self.page_size, self.pages, self.heads, self.dim)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, dim: int,
+              dtype: torch.dtype = torch.bfloat16, device=None) -> "KVCache":
+        device = torch.device("cuda") if device is None else device
+        shape = (int(pages), int(heads), int(page_size), int(dim))
+        return cls(torch.empty(shape, dtype=dtype, device=device),
+                   torch.empty(shape, dtype=dtype, device=device))
+
+    @property
+    def dtype(self):
+        return self.k.dtype
+
+    @property
+    def device(self):
+        return self.k.device
+
+
+def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                  positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                  q: Optional[torch.Tensor] = None,
+                  q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Store k and v ([T][heads][dim], slices allowed, fp32 or the cache's
+    type) at slots ([T] int64, page * page_size + row; -1 is padding), keys
+    rotated by `rope`; with q, the rotated queries are returned in the cache's
+    type.  One launch."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    dev = cache.device
+    kv = _need_heads(k, "k", (torch.float32, cache.dtype), dev)
+    vv = _need_heads(v, "v", (k.dtype,), dev)
+    T = int(k.shape[0])
+    _need_shape(k, "k", (T, cache.heads, cache.dim))
+    _need_shape(v, "v", (T, cache.heads, cache.dim))
+    _need(slots, "slots", (torch.int64,), dev)
+    _need_shape(slots, "slots", (T,))
+    spec = None
+    if rope is not None:
+        if not isinstance(rope, Rope):
+            raise TypeError("rope must be a Rope")
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        rope._need_positions(positions, T, dev)
+        spec = rope._spec[0]
+    qv = ov = None
+    Hq = 0
+    if q is not None:
+        qv = _need_heads(q, "q", (k.dtype,), dev)
+        Hq = int(q.shape[1])
+        _need_shape(q, "q", (T, Hq, cache.dim))
+        if q_out is None:
+            q_out = torch.empty((T, Hq, cache.dim), dtype=cache.dtype, device=dev)
+        ov = _need_heads(q_out, "q_out", (cache.dtype,), dev)
+        _need_shape(q_out, "q_out", (T, Hq, cache.dim))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _launch(dev, "pq1_kv_append", load_library().pq1_kv_append, kv, vv, _ptr(slots), qv, ov, Hq,
+            None if spec is None else _ptr(positions), None if spec is None else _ptr(rope.freqs),
+            spec, cache._struct, T)
+    return q_out
+
+
+# Attention workspaces, one per (device, stream), grown on demand; kept apart
+# from the GEMV's, whose counter region must stay as its calls leave it.
+_attn_ws = {}
+
+
+def attention_workspace(need: int, device: torch.device) -> torch.Tensor:
+    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    with _ws_lock:
+        ws = _attn_ws.get(key)
+        if ws is None or ws.numel() < need:
+            if ws is not None:
+                # a graph captured earlier may still hold the old buffer's address
+                _ws_retired.append(ws)
+            ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=device)
+            _attn_ws[key] = ws
+        return ws
+
+
+def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
+                        cu_q: torch.Tensor, kv_len: torch.Tensor, max_q: int, max_kv: int,
+                        scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                        out: Optional[torch.Tensor] = None,
+                        out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """Attention of the new tokens q [T][Hq][dim] of B sequences over the
+    cache (include/pq1.h, pq1_paged_attention).
+
+    page_table [B][max_pages], cu_q [B+1] and kv_len [B] are int32 on the GPU;
+    max_q and max_kv are the longest chunk and kv_len, known on the host.
+    scale defaults to dim^-0.5.  out (of q's type, or fp32) is new unless
+    given; rows that no sequence owns keep what they held."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    dev = cache.device
+    qv = _need_heads(q, "q", (cache.dtype,), dev)
+    T, Hq, D = (int(n) for n in q.shape)
+    _need_shape(q, "q", (T, Hq, cache.dim))
+    _need(page_table, "page_table", (torch.int32,), dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D, [sequences][pages]")
+    B, max_pages = (int(n) for n in page_table.shape)
+    _need(cu_q, "cu_q", (torch.int32,), dev)
+    _need_shape(cu_q, "cu_q", (B + 1,))
+    _need(kv_len, "kv_len", (torch.int32,), dev)
+    _need_shape(kv_len, "kv_len", (B,))
+    if out is None:
+        dt = cache.dtype if out_dtype is None else out_dtype
+        if dt not in (cache.dtype, torch.float32):
+            raise TypeError(f"out_dtype must be {cache.dtype} or torch.float32")
+        out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
+    ov = _need_heads(out, "out", (cache.dtype, torch.float32), dev)
+    _need_shape(out, "out", (T, Hq, D))
+    lib = load_library()
+    max_q, max_kv = int(max_q), int(max_kv)
+    need = lib.pq1_paged_attention_workspace_bytes(B, T, Hq, cache.heads, D, max_q, max_kv)
+    ws = attention_workspace(need, dev) if need else None
+    _launch(dev, "pq1_paged_attention", lib.pq1_paged_attention, qv, ov, cache._struct,
+            _ptr(page_table), max_pages, _ptr(cu_q), _ptr(kv_len), B, T, Hq, max_q, max_kv,
+            D ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window),
+            _ptr(ws), need)
+    return out

@@ -78,6 +78,10 @@ typedef struct {
  * 8c + 2q + t (c, q < 4, t < 2) holds the element at offset 4c + q + 16t. */
 enum { PQ1_F32 = 0, PQ1_BF16 = 1, PQ1_BF16_GEMM = 2 };
 
+/* Further element type of the attention-layer calls at the end of this file
+ * (pq1_rotate does not take it). */
+enum { PQ1_F16 = 3 };
+
 /* Layout of the bf16 activation of pq1_gemm_ex. */
 enum { PQ1_X_ROW_MAJOR = 0, PQ1_X_GEMM_ORDER = 1 };
 
@@ -334,6 +338,151 @@ pq1_status pq1_gemm_ex(const uint16_t* x_rot_bf16, const uint32_t* w_bits, const
  *            inputs).  K a multiple of 1024, M * K < 2^31. */
 pq1_status pq1_embed(const int32_t* tokens, int64_t M, const uint32_t* w_bits, const float* scales,
                      const float* signs, float* out, int64_t V, int64_t K, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention layer: what stands between the projections of a layer.  Queries
+ * and keys are rotated by their positions, new keys and values go into a
+ * paged cache, and the new tokens attend over the cache.  The three calls
+ * enqueue on `stream`, allocate nothing, keep nothing between calls and may
+ * be captured into a graph.
+ *
+ * Element types here are PQ1_F32, PQ1_BF16 and PQ1_F16.  Sums, softmax
+ * statistics and rotations are computed in fp32 (angles in fp64) and rounded
+ * once when stored, to nearest, ties to even.
+ * ------------------------------------------------------------------------- */
+
+/* A [tokens][heads][dim] array whose head vectors are contiguous: element
+ * (t, h, d) is at data[t * token_stride + h * head_stride + d] (strides in
+ * elements, not negative).  A slice of a stacked projection's output is such
+ * an array.  data is 16-byte aligned and both strides are multiples of 16
+ * bytes (PQ1_ERR_ALIGN). */
+typedef struct {
+    void* data;
+    int32_t dtype;
+    int64_t token_stride;
+    int64_t head_stride;
+} pq1_heads;
+
+/* Rotation by positions on 1 to 4 axes (text position; or time, height and
+ * width of an image or video).  The first `rot` elements of a head form
+ * rot / 2 pairs; pair i is turned by the angle p[a(i)] * freqs[i], where p is
+ * the token's position on each axis and a(i) the axis that owns the pair:
+ *   (y0, y1) = (x0 cos - x1 sin, x1 cos + x0 sin);
+ * elements rot .. dim-1 are copied.
+ *   rot          even, 2 <= rot <= dim.
+ *   axes         1 .. 4.
+ *   section      pairs that each axis owns; their sum is rot / 2, unused
+ *                entries are ignored.
+ *   interleaved  0: axis 0 owns the first section[0] pairs, axis 1 the next
+ *                section[1], and so on.  1: pair i belongs to axis i % axes as
+ *                long as i / axes < section[i % axes], and to axis 0 after
+ *                that (every axis must find its pairs: a + axes *
+ *                (section[a] - 1) < rot / 2 for a > 0).
+ *   pairing      PQ1_ROPE_HALVES: pair i is elements (i, i + rot / 2);
+ *                PQ1_ROPE_ADJACENT: elements (2i, 2i + 1).
+ *   inverse      1 turns by the negative angle: the inverse of the rotation
+ *                and, as it is orthogonal, its gradient.
+ * A value outside these gives PQ1_ERR_SHAPE (rot, axes, section) or
+ * PQ1_ERR_ARG (the flags). */
+typedef struct {
+    int32_t rot;
+    int32_t axes;
+    int32_t section[4];
+    int32_t interleaved;
+    int32_t pairing;
+    int32_t inverse;
+} pq1_rope_spec;
+enum { PQ1_ROPE_HALVES = 0, PQ1_ROPE_ADJACENT = 1 };
+
+/* A paged key/value cache: k and v are [pages][heads][page_size][dim], bf16
+ * or f16, contiguous, 16-byte aligned.  Slot s is row s % page_size of page
+ * s / page_size.  page_size is a power of two up to 65536; dim is a multiple
+ * of 8 up to 1024; heads up to 1024. */
+typedef struct {
+    void* k;
+    void* v;
+    int32_t dtype;
+    int32_t page_size;
+    int64_t pages;
+    int32_t heads;
+    int32_t dim;
+} pq1_kv_cache;
+
+/* y = rotation of x, for T tokens of H heads of D elements.
+ *   x, y       views of the input and the output, of any of the three types;
+ *              y may be x itself (same data, type and strides), else they may
+ *              not overlap.
+ *   positions  [axes][T] int32, of any sign (4-byte aligned).
+ *   freqs      [rot / 2] fp64, radians per position (8-byte aligned).
+ *   T >= 0 (0 does nothing), H >= 1, D a multiple of 8 up to 1024.
+ * Angles are reduced in fp64: a position of any size loses nothing beyond the
+ * fp32 rounding of the reduced angle. */
+pq1_status pq1_rope(const pq1_heads* x, const pq1_heads* y, const int32_t* positions,
+                    const double* freqs, const pq1_rope_spec* spec, int64_t T, int32_t H,
+                    int32_t D, void* stream);
+
+/* Append T tokens to the cache and rotate keys (and queries) on the way, in
+ * one launch: row slots[t] of every page head gets the rotated key and the
+ * value of token t.
+ *   k, v       [T][cache heads][cache dim] views of one type, fp32 or the
+ *              cache's.
+ *   slots      [T] int64 (8-byte aligned).  A token whose slot is outside
+ *              [0, pages * page_size) is not stored (-1 marks padding).  Live
+ *              slots must differ from one another.
+ *   q, q_out   NULL, or views of [T][Hq][cache dim]: q of k's type, q_out of
+ *              the cache's; every row of q_out is written, also for tokens
+ *              that are not stored.  Hq is ignored when q is NULL.
+ *   positions, freqs, spec   as in pq1_rope; spec NULL stores (and copies q)
+ *              without rotation, positions and freqs are then ignored.
+ * Inputs may overlap one another, outputs may overlap nothing. */
+pq1_status pq1_kv_append(const pq1_heads* k, const pq1_heads* v, const int64_t* slots,
+                         const pq1_heads* q, const pq1_heads* q_out, int32_t Hq,
+                         const int32_t* positions, const double* freqs,
+                         const pq1_rope_spec* spec, const pq1_kv_cache* cache, int64_t T,
+                         void* stream);
+
+/* Attention of the new tokens of B sequences over the cache.  Sequence b owns
+ * rows cu_q[b] .. cu_q[b+1]-1 of q and out, its n newest tokens; its keys are
+ * rows 0 .. kv_len[b]-1 of the pages page_table[b][0], [1], ..., the new
+ * tokens' own among them (they were appended before).  Row i stands at
+ * position p = kv_len[b] - n + i and
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * over the keys j it sees: with causal != 0 those with j <= p, and with
+ * window > 0 only those with j > p - window as well; else all.  Query head h
+ * uses cache head h / (Hq / heads).  A row that sees no key gives zeros.
+ *   q          [T][Hq][dim] of the cache's type; out of that type or fp32.
+ *   page_table [B][max_pages] int32; entries past a sequence's last visible
+ *              page are not read.  A page id outside [0, pages), or a key at
+ *              or past max_pages * page_size, gives NaN in the rows that see
+ *              it (nothing outside the cache is read).
+ *   cu_q       [B+1] int32, not decreasing, within [0, T] (values outside are
+ *              clamped).  Rows of out that no sequence owns are not written.
+ *   kv_len     [B] int32.
+ *   max_q, max_kv   the longest chunk and the longest kv_len of the batch, as
+ *              the caller knows them on the host: they shape the launch and
+ *              the workspace, and results are right (if slower) for others.
+ *   scale      > 0 and finite.
+ *   window     >= 0, 0 for none; only with causal.
+ *   workspace  pq1_paged_attention_workspace_bytes(...) bytes, 256-byte
+ *              aligned; may be NULL where that is 0.  Its content does not
+ *              matter and is not kept; calls that may overlap in time need
+ *              different workspaces.
+ *   dim is 64, 128 or 256; Hq a multiple of the cache's heads; T * Hq and the
+ *   pages' row count (pages * heads * page_size) below 2^31 and 2^40.
+ * Results do not depend on scheduling: the key range is split by the call's
+ * sizes alone and the parts are joined in order.  Probabilities are rounded
+ * to the cache's type for the second product, as its matrix instructions
+ * take them; products are summed in fp32. */
+pq1_status pq1_paged_attention(const pq1_heads* q, const pq1_heads* out,
+                               const pq1_kv_cache* cache, const int32_t* page_table,
+                               int64_t max_pages, const int32_t* cu_q, const int32_t* kv_len,
+                               int64_t B, int64_t T, int32_t Hq, int64_t max_q, int64_t max_kv,
+                               float scale, int32_t causal, int32_t window, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for the call above (0: none needed, or invalid sizes). */
+size_t pq1_paged_attention_workspace_bytes(int64_t B, int64_t T, int32_t Hq, int32_t heads,
+                                           int32_t dim, int64_t max_q, int64_t max_kv);
 
 /* Static description of a status code (never NULL). */
 const char* pq1_status_str(pq1_status s);
