@@ -77,7 +77,11 @@ struct AttnArgs {
 
 // How a call is cut into workgroups: a function of its sizes alone.
 struct AttnPlan {
-  int64_t row_tiles = 0;  // workgroups along the rows of one (sequence, cache head)
+  int64_t tokens = 0;     // new tokens of the longest chunk
+  int row_blocks = 1;     // 16-row blocks of a row tile
+  int64_t row_tiles = 0;  // row tiles of one (sequence, cache head)
+  int nsplit = 1;         // parts of the keys
+  int chunk = 0;          // keys of a part
   size_t workspace_bytes = 0;
   bool fits = false;      // the grid is launchable
 };

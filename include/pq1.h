@@ -457,7 +457,7 @@ pq1_status pq1_kv_append(const pq1_heads* k, const pq1_heads* v, const int64_t* 
  *              it (nothing outside the cache is read).
  *   cu_q       [B+1] int32, not decreasing, within [0, T] (values outside are
  *              clamped).  Rows of out that no sequence owns are not written.
- *   kv_len     [B] int32.
+ *   kv_len     [B] int32, at most 0x7fff0000 (clamped; negative counts as 0).
  *   max_q, max_kv   the longest chunk and the longest kv_len of the batch, as
  *              the caller knows them on the host: they shape the launch and
  *              the workspace, and results are right (if slower) for others.
