@@ -607,8 +607,7 @@ def pq1_rotate_gemv_packed_noalloc(x: torch.Tensor, signs: torch.Tensor, pw: Pac
         _check(lib.pq1_rotate_gemv_packed_noalloc(_ptr(x), _ptr(signs), _perm(perm), _ptr(pw.bits),
                                                   _ptr(pw.scales), _scale_code(pw.scale_dtype),
                                                   _ptr(out), pw.N, x.numel(), _stream(dev)),
-               "pq1_rotate_gemv_packed_noalloc", "pq1_rope", "pq1_kv_append",
-           "pq1_paged_attention", "pq1_paged_attention_workspace_bytes")
+               "pq1_rotate_gemv_packed_noalloc")
     return out
 
 
