@@ -42,12 +42,15 @@ BENCH_LIB = os.path.join(PKG, "libpq1_bench.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.hip", "rotate.hip", "gemv.hip", "gemv_packed.hip", "gemm.hip", "gemm_skinny.hip",
-           "api_attention.hip", "rope.hip", "paged_attention.hip"]
+           "api_attention.hip", "rope.hip", "paged_attention.hip",
+           "paged_attention_tiles.hip"]
 BENCH_SOURCES = ["bench_kernels.hip"]
 
 # gemm_skinny.hip: MFMA results stay in ordinary VGPRs (the per-group fold
 # reads them right away; the accumulator-register form cost a copy each).
-SOURCE_FLAGS: dict = {"gemm_skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# paged_attention_tiles.hip: likewise, scores and outputs are read by the softmax.
+SOURCE_FLAGS: dict = {"gemm_skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+                      "paged_attention_tiles.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=fast",

@@ -75,10 +75,13 @@ struct AttnArgs {
   int window = 0;
 };
 
+constexpr int kTileRows = 256;  // rows of a many-rows tile
+
 // How a call is cut into workgroups: a function of its sizes alone.
 struct AttnPlan {
   int64_t tokens = 0;     // new tokens of the longest chunk
-  int row_blocks = 1;     // 16-row blocks of a row tile
+  bool many = false;      // tiles of many rows (paged_attention_tiles.hip)
+  int tile_rows = 16;     // rows of a row tile
   int64_t row_tiles = 0;  // row tiles of one (sequence, cache head)
   int nsplit = 1;         // parts of the keys
   int chunk = 0;          // keys of a part
@@ -87,6 +90,8 @@ struct AttnPlan {
 };
 AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_q,
                         int64_t max_kv);
+hipError_t launch_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
+                            void* workspace, hipStream_t s);
 hipError_t launch_attention(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
                             void* workspace, hipStream_t s);
 

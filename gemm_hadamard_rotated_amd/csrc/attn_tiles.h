@@ -1,0 +1,169 @@
+// Device pieces shared by the attention kernels (paged_attention.hip: few rows;
+// paged_attention_tiles.hip: tiles of many rows): which keys a row sees, how a
+// row tile's keys are split, matrix-core products, probabilities as two-byte
+// numbers, and the handling of infinities and NaN.
+#pragma once
+
+#include "attn_device.h"
+#include "attn_internal.h"
+
+namespace pq1 {
+
+constexpr float kNegInf = -__builtin_inff();
+
+constexpr int kMaxKeys = 0x7fff0000;  // of a sequence: key numbers plus a tile stay in 31 bits
+
+// What a workgroup needs to know of its sequence.
+struct Seq {
+  int64_t q0;  // first row of q
+  int n;       // new tokens
+  int kv;      // keys
+};
+
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int64_t b) {
+  int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+  q0 = q0 < 0 ? 0 : q0 > a.T ? a.T : q0;
+  q1 = q1 < q0 ? q0 : q1 > a.T ? a.T : q1;
+  const int kv = a.kv_len[b];
+  return {q0, static_cast<int>(q1 - q0), kv < 0 ? 0 : kv > kMaxKeys ? kMaxKeys : kv};
+}
+
+// Keys [lo, hi) that row i sees.
+__device__ __forceinline__ void visible(const AttnArgs& a, const Seq& s, int i, int* lo, int* hi) {
+  *lo = 0;
+  *hi = s.kv;
+  if (a.causal) {
+    const int64_t end = static_cast<int64_t>(s.kv) - s.n + i + 1;
+    *hi = end < 0 ? 0 : static_cast<int>(end);
+    if (a.window > 0 && *hi > a.window) *lo = *hi - a.window;
+  }
+}
+
+// Rows of one (sequence, cache head) are numbered r = i * G + g over its new
+// tokens i and the G query heads of the cache head, so that all of them share
+// the keys and values a workgroup reads.  A tile of such rows sees keys
+// [start, hi); they are cut into parts of `chunk` keys.
+struct Parts {
+  int start;  // rounded down to a key tile
+  int lo, hi;  // keys that some row sees
+  int lo_max, hi_min;  // keys in [lo_max, hi_min) are seen by every row
+  int chunk;
+  int count;
+};
+
+__device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int r0, int rows,
+                                            int chunk, int nsplit) {
+  const int last = s.n * a.G - 1;
+  const int i0 = r0 / a.G, i1 = (r0 + rows - 1 < last ? r0 + rows - 1 : last) / a.G;
+  Parts p;
+  int lo0, hi0, lo1, hi1;
+  visible(a, s, i0, &lo0, &hi0);
+  visible(a, s, i1, &lo1, &hi1);
+  p.start = lo0 & ~31;
+  p.lo = lo0;
+  p.hi = hi1;
+  p.lo_max = lo1;
+  p.hi_min = hi0;
+  const int64_t keys = p.hi > p.start ? static_cast<int64_t>(p.hi) - p.start : 0;
+  // a cache longer than the caller said stretches the parts
+  const int64_t need = (keys + nsplit - 1) / nsplit;
+  p.chunk = need > chunk ? static_cast<int>((need + 31) & ~int64_t{31}) : chunk;
+  p.count = static_cast<int>((keys + p.chunk - 1) / p.chunk);
+  return p;
+}
+
+template <typename T>
+using Vec8 = __attribute__((ext_vector_type(8))) T;
+using F4 = __attribute__((ext_vector_type(4))) float;
+using U4 = __attribute__((ext_vector_type(4))) uint32_t;
+using U2 = __attribute__((ext_vector_type(2))) uint32_t;
+
+__device__ __forceinline__ F4 mfma16(U4 a, U4 b, F4 c, bf16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(Vec8<bf16>, a),
+                                                 __builtin_bit_cast(Vec8<bf16>, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ F4 mfma16(U4 a, U4 b, F4 c, f16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(Vec8<f16>, a),
+                                                __builtin_bit_cast(Vec8<f16>, b), c, 0, 0, 0);
+}
+
+// Maximum and sum over the lanes that share lane % 16.
+__device__ __forceinline__ float max_groups(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_groups(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Probabilities are carried times 2^kUp, which the division by their sum
+// takes out again: an f16 then holds those down to 2^-22 of the largest in
+// full.  The running maximum may lag behind by kLag (fewer rescalings of the
+// sums); 2^(kUp + kLag) is within f16.
+constexpr float kUp = 8.0f, kLag = 6.0f;
+
+// A probability as NP two-byte numbers whose sum it is: one where the result
+// is rounded to that type anyway; for an fp32 result three bf16 or two f16,
+// which hold all 24 or 22 bits.  There each number is cut off, not rounded,
+// and what is left is kept above zero (by less than 2^-32 of the largest
+// probability), so that every part of a seen key's probability is positive and
+// an infinite value gives an infinity, not the difference of two.
+template <typename T, typename TO>
+constexpr int kParts = sizeof(TO) == 2 ? 1 : __is_same(T, bf16) ? 3 : 2;
+
+template <typename T, int NP>
+__device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) {
+  if constexpr (NP == 1) {
+    Vec8<T> v;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = static_cast<T>(p[t]);
+    out[0] = __builtin_bit_cast(U4, v);
+  } else {
+    constexpr float least = __is_same(T, bf16) ? 0x1p-126f : 0x1p-24f;
+    float r[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) r[t] = p[t];
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        float& x = r[2 * w];
+        float& y = r[2 * w + 1];
+        float cx, cy;
+        if constexpr (__is_same(T, bf16)) {
+          const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+          out[n][w] = __builtin_amdgcn_perm(uy, ux, 0x07060302u);
+          cx = __uint_as_float(ux & 0xffff0000u);
+          cy = __uint_as_float(uy & 0xffff0000u);
+        } else {
+          const auto c = __builtin_amdgcn_cvt_pkrtz(x, y);
+          out[n][w] = __builtin_bit_cast(uint32_t, c);
+          cx = static_cast<float>(c[0]);
+          cy = static_cast<float>(c[1]);
+        }
+        if (n + 1 < NP) {
+          x = fmaxf(x - cx, fminf(p[2 * w], least));
+          y = fmaxf(y - cy, fminf(p[2 * w + 1], least));
+        }
+      }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ bool not_finite(uint32_t pair) {  // either of two elements
+  constexpr uint32_t e = __is_same(T, bf16) ? 0x7f80u : 0x7c00u;
+  return (pair & e) == e || (pair & (e << 16)) == (e << 16);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
+  constexpr uint32_t e = __is_same(T, bf16) ? 0x7f80u : 0x7c00u;
+  return ((pair & e) == e ? 0u : pair & 0xffffu) |
+         ((pair & (e << 16)) == (e << 16) ? 0u : pair & 0xffff0000u);
+}
+
+}  // namespace pq1

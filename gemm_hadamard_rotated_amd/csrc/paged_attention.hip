@@ -4,145 +4,11 @@
 //   o = sum_j 2^(c q.k_j - m) v_j / sum_j 2^(c q.k_j - m),   c = scale log2(e),
 // with a running maximum m over tiles of keys, so that one pass over the
 // cache does: a tile with a larger maximum scales what was summed so far.
-#include "attn_device.h"
-#include "attn_internal.h"
+#include "attn_tiles.h"
 
 namespace pq1 {
 
 namespace {
-
-constexpr float kNegInf = -__builtin_inff();
-
-constexpr int kMaxKeys = 0x7fff0000;  // of a sequence: key numbers plus a tile stay in 31 bits
-
-// What a workgroup needs to know of its sequence.
-struct Seq {
-  int64_t q0;  // first row of q
-  int n;       // new tokens
-  int kv;      // keys
-};
-
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int64_t b) {
-  int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
-  q0 = q0 < 0 ? 0 : q0 > a.T ? a.T : q0;
-  q1 = q1 < q0 ? q0 : q1 > a.T ? a.T : q1;
-  const int kv = a.kv_len[b];
-  return {q0, static_cast<int>(q1 - q0), kv < 0 ? 0 : kv > kMaxKeys ? kMaxKeys : kv};
-}
-
-// Keys [lo, hi) that row i sees.
-__device__ __forceinline__ void visible(const AttnArgs& a, const Seq& s, int i, int* lo, int* hi) {
-  *lo = 0;
-  *hi = s.kv;
-  if (a.causal) {
-    const int64_t end = static_cast<int64_t>(s.kv) - s.n + i + 1;
-    *hi = end < 0 ? 0 : static_cast<int>(end);
-    if (a.window > 0 && *hi > a.window) *lo = *hi - a.window;
-  }
-}
-
-// Rows of one (sequence, cache head) are numbered r = i * G + g over its new
-// tokens i and the G query heads of the cache head, so that all of them share
-// the keys and values a workgroup reads.  A tile of such rows sees keys
-// [start, hi); they are cut into parts of `chunk` keys.
-struct Parts {
-  int start;  // rounded down to a key tile
-  int lo, hi;  // keys that some row sees
-  int lo_max, hi_min;  // keys in [lo_max, hi_min) are seen by every row
-  int chunk;
-  int count;
-};
-
-__device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int r0, int rows,
-                                            int chunk, int nsplit) {
-  const int last = s.n * a.G - 1;
-  const int i0 = r0 / a.G, i1 = (r0 + rows - 1 < last ? r0 + rows - 1 : last) / a.G;
-  Parts p;
-  int lo0, hi0, lo1, hi1;
-  visible(a, s, i0, &lo0, &hi0);
-  visible(a, s, i1, &lo1, &hi1);
-  p.start = lo0 & ~31;
-  p.lo = lo0;
-  p.hi = hi1;
-  p.lo_max = lo1;
-  p.hi_min = hi0;
-  const int64_t keys = p.hi > p.start ? static_cast<int64_t>(p.hi) - p.start : 0;
-  // a cache longer than the caller said stretches the parts
-  const int64_t need = (keys + nsplit - 1) / nsplit;
-  p.chunk = need > chunk ? static_cast<int>((need + 31) & ~int64_t{31}) : chunk;
-  p.count = static_cast<int>((keys + p.chunk - 1) / p.chunk);
-  return p;
-}
-
-template <typename T>
-using Vec8 = __attribute__((ext_vector_type(8))) T;
-using F4 = __attribute__((ext_vector_type(4))) float;
-using U4 = __attribute__((ext_vector_type(4))) uint32_t;
-using U2 = __attribute__((ext_vector_type(2))) uint32_t;
-
-__device__ __forceinline__ F4 mfma16(U4 a, U4 b, F4 c, bf16) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(Vec8<bf16>, a),
-                                                 __builtin_bit_cast(Vec8<bf16>, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ F4 mfma16(U4 a, U4 b, F4 c, f16) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(Vec8<f16>, a),
-                                                __builtin_bit_cast(Vec8<f16>, b), c, 0, 0, 0);
-}
-
-// Maximum and sum over the lanes that share lane % 16.
-__device__ __forceinline__ float max_groups(float x) {
-  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float sum_groups(float x) {
-  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
-// Probabilities are carried times 2^kUp, which the division by their sum
-// takes out again: an f16 then holds those down to 2^-22 of the largest in
-// full.  The running maximum may lag behind by kLag (fewer rescalings of the
-// sums); 2^(kUp + kLag) is within f16.
-constexpr float kUp = 8.0f, kLag = 6.0f;
-
-// A probability as NP two-byte numbers whose sum it is: one where the result
-// is rounded to that type anyway; for an fp32 result three bf16 or two f16,
-// which hold all 24 or 22 bits.
-template <typename T, typename TO>
-constexpr int kParts = sizeof(TO) == 2 ? 1 : __is_same(T, bf16) ? 3 : 2;
-
-template <typename T, int NP>
-__device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) {
-  float r[8];
-#pragma unroll
-  for (int t = 0; t < 8; ++t) r[t] = p[t];
-#pragma unroll
-  for (int n = 0; n < NP; ++n) {
-    Vec8<T> v;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      v[t] = static_cast<T>(r[t]);
-      if (n + 1 < NP) r[t] -= static_cast<float>(v[t]);
-    }
-    out[n] = __builtin_bit_cast(U4, v);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ bool not_finite(uint32_t pair) {  // either of two elements
-  constexpr uint32_t e = __is_same(T, bf16) ? 0x7f80u : 0x7c00u;
-  return (pair & e) == e || (pair & (e << 16)) == (e << 16);
-}
-template <typename T>
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
-  constexpr uint32_t e = __is_same(T, bf16) ? 0x7f80u : 0x7c00u;
-  return ((pair & e) == e ? 0u : pair & 0xffffu) |
-         ((pair & (e << 16)) == (e << 16) ? 0u : pair & 0xffff0000u);
-}
 
 // ---------------------------------------------------------------------------
 // Few rows: 16 RB rows of one (sequence, cache head) and one part of its keys
@@ -574,28 +440,48 @@ hipError_t launch_few(const AttnPlan& plan, const AttnArgs& a, void* workspace, 
     few_rows_kernel<T, TO, D, RB, true><<<grid, 64 * kWaves, 0, s>>>(a, fg, part_o, part_ml);
   else
     few_rows_kernel<T, TO, D, RB, false><<<grid, 64 * kWaves, 0, s>>>(a, fg, part_o, part_ml);
-  if (plan.nsplit > 1) {
-    const dim3 jg(static_cast<uint32_t>(a.B * plan.tokens * ((a.Hk * a.G + 3) / 4)));
-    join_kernel<TO, D><<<jg, 256, 0, s>>>(a, fg, 16 * RB, static_cast<int>(plan.tokens), part_o,
-                                          part_ml);
-  }
+  return hipGetLastError();
+}
+
+template <typename TO, int D>
+hipError_t launch_join(const AttnPlan& plan, const AttnArgs& a, void* workspace, hipStream_t s) {
+  const FewGrid fg{static_cast<int>(plan.row_tiles), plan.nsplit, plan.chunk};
+  const float* part_o = static_cast<const float*>(workspace);
+  const float2* part_ml = reinterpret_cast<const float2*>(
+      part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
+  const dim3 grid(static_cast<uint32_t>(a.B * plan.tokens * ((a.Hk * a.G + 3) / 4)));
+  join_kernel<TO, D><<<grid, 256, 0, s>>>(a, fg, plan.tile_rows, static_cast<int>(plan.tokens),
+                                          part_o, part_ml);
   return hipGetLastError();
 }
 
 template <typename T, typename TO, int D>
 hipError_t launch_rows(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStream_t s) {
-  return plan.row_blocks == 1 ? launch_few<T, TO, D, 1>(plan, a, ws, s)
+  return plan.tile_rows == 16 ? launch_few<T, TO, D, 1>(plan, a, ws, s)
                               : launch_few<T, TO, D, 2>(plan, a, ws, s);
 }
 
 template <typename T, typename TO>
-hipError_t launch_dim(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_few_rows(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStream_t s) {
   switch (a.D) {
     case 64: return launch_rows<T, TO, 64>(plan, a, ws, s);
     case 128: return launch_rows<T, TO, 128>(plan, a, ws, s);
     default: return launch_rows<T, TO, 256>(plan, a, ws, s);
   }
 }
+
+template <typename TO>
+hipError_t join_parts(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStream_t s) {
+  switch (a.D) {
+    case 64: return launch_join<TO, 64>(plan, a, ws, s);
+    case 128: return launch_join<TO, 128>(plan, a, ws, s);
+    default: return launch_join<TO, 256>(plan, a, ws, s);
+  }
+}
+
+// A sequence's longest chunk has up to this many rows of a cache head in the
+// few-rows kernel, more in the many-rows one.
+constexpr int64_t kFewRows = 64;
 
 }  // namespace
 
@@ -604,8 +490,9 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max
   AttnPlan p;
   p.tokens = max_q < 1 ? 1 : max_q < T ? max_q : T;
   const int64_t rows = p.tokens * (Hq / Hk);
-  p.row_blocks = rows <= 16 ? 1 : 2;
-  p.row_tiles = (rows + 16 * p.row_blocks - 1) / (16 * p.row_blocks);
+  p.many = rows > kFewRows;
+  p.tile_rows = p.many ? kTileRows : rows <= 16 ? 16 : 32;
+  p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   // Parts: enough workgroups for two on each of the 256 CUs, but no part
   // shorter than one key tile for each wave.
   const int64_t kv = max_kv < 1 ? 1 : max_kv > 0x7fffffff ? 0x7fffffff : max_kv;
@@ -625,11 +512,21 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max
 
 hipError_t launch_attention(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
                             void* workspace, hipStream_t s) {
-  if (dtype == PQ1_BF16)
-    return out_dtype == PQ1_F32 ? launch_dim<bf16, float>(plan, a, workspace, s)
-                                : launch_dim<bf16, bf16>(plan, a, workspace, s);
-  return out_dtype == PQ1_F32 ? launch_dim<f16, float>(plan, a, workspace, s)
-                              : launch_dim<f16, f16>(plan, a, workspace, s);
+  hipError_t e;
+  if (plan.many)
+    e = launch_many_rows(plan, a, dtype, out_dtype, workspace, s);
+  else if (dtype == PQ1_BF16)
+    e = out_dtype == PQ1_F32 ? launch_few_rows<bf16, float>(plan, a, workspace, s)
+                             : launch_few_rows<bf16, bf16>(plan, a, workspace, s);
+  else
+    e = out_dtype == PQ1_F32 ? launch_few_rows<f16, float>(plan, a, workspace, s)
+                             : launch_few_rows<f16, f16>(plan, a, workspace, s);
+  if (e != hipSuccess || plan.nsplit == 1) return e;
+  switch (out_dtype) {
+    case PQ1_BF16: return join_parts<bf16>(plan, a, workspace, s);
+    case PQ1_F16: return join_parts<f16>(plan, a, workspace, s);
+    default: return join_parts<float>(plan, a, workspace, s);
+  }
 }
 
 }  // namespace pq1

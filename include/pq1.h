@@ -470,9 +470,12 @@ pq1_status pq1_kv_append(const pq1_heads* k, const pq1_heads* v, const int64_t* 
  *   dim is 64, 128 or 256; Hq a multiple of the cache's heads; T * Hq and the
  *   pages' row count (pages * heads * page_size) below 2^31 and 2^40.
  * Results do not depend on scheduling: the key range is split by the call's
- * sizes alone and the parts are joined in order.  Probabilities are rounded
- * to the cache's type for the second product, as its matrix instructions
- * take them; products are summed in fp32. */
+ * sizes alone and the parts are joined in order.  Probabilities enter the
+ * second product as the cache's type (for an fp32 result as two or three such
+ * numbers, which hold at least 22 bits), as its matrix instructions take them;
+ * products are summed in fp32.  An infinity or NaN in a key or value reaches
+ * the rows that see it (an infinity as itself, or as NaN where its probability
+ * rounds to zero) and no others. */
 pq1_status pq1_paged_attention(const pq1_heads* q, const pq1_heads* out,
                                const pq1_kv_cache* cache, const int32_t* page_table,
                                int64_t max_pages, const int32_t* cu_q, const int32_t* kv_len,
