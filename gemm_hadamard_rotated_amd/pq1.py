@@ -669,28 +669,54 @@ _FLOATS = tuple(_TYPE_CODE)
 _PAIRINGS = {"halves": PQ1_ROPE_HALVES, "adjacent": PQ1_ROPE_ADJACENT}
 
 
-def _need_heads(t: torch.Tensor, name: str, dtypes, dev=None) -> Pq1Heads:
+# These calls are small and frequent (one decoded token: three of them a
+# layer), so their path through Python is kept short: addresses go as plain
+# integers, the stream comes from torch's raw accessor (0.1 us; a Stream object
+# takes 2), and what a Rope or a KVCache can check is checked when it is made.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _need_heads(t: torch.Tensor, name: str, dtypes, dev=None, shape=None) -> Pq1Heads:
     """A [tokens][heads][dim] tensor with contiguous head vectors, as the
     library's view of it."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (no CPU path exists)")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
-    if t.dim() != 3:
+    dt = t.dtype
+    if dt not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {dt}")
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
+    if len(size) != 3:
         raise ValueError(f"{name} must be 3-D, [tokens][heads][dim]")
     ts, hs, ds = t.stride()
-    if ds != 1 and t.shape[2] != 1:
+    if ds != 1 and size[2] != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
     # the stride of an axis of length one says nothing
-    if t.shape[0] <= 1:
-        ts = 0
-    if t.shape[1] <= 1:
-        hs = 0
-    return Pq1Heads(t.data_ptr(), _TYPE_CODE[t.dtype], ts, hs)
+    return Pq1Heads(t.data_ptr(), _TYPE_CODE[dt], ts if size[0] > 1 else 0,
+                    hs if size[1] > 1 else 0)
+
+
+def _need_vector(t: torch.Tensor, name: str, dtype: torch.dtype, dev, shape) -> int:
+    """The address of a contiguous tensor of this type and shape on dev."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU (no CPU path exists)")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _need_shape(t: torch.Tensor, name: str, shape):
@@ -700,12 +726,14 @@ def _need_shape(t: torch.Tensor, name: str, shape):
 
 def _launch(dev: torch.device, where: str, fn, *args):
     """fn(*args, current stream of dev) with dev current."""
-    if torch.cuda.current_device() == dev.index:
-        code = fn(*args, _stream(dev))
+    index = dev.index
+    if _current_device() == index:
+        code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, _stream(dev))
-    _check(code, where)
+            code = fn(*args, _raw_stream(index))
+    if code != PQ1_OK:
+        _check(code, where)
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -742,13 +770,15 @@ class Rope:
             Pq1RopeSpec(rot, len(sections), (ctypes.c_int32 * 4)(*padded), int(bool(interleaved)),
                         _PAIRINGS[pairing], inverse) for inverse in (0, 1))
 
-    def _need_positions(self, positions: torch.Tensor, T: int, dev):
-        _need(positions, "positions", (torch.int32,), dev)
-        _need_numel(positions, "positions", self.axes * T)
-        if positions.dim() != 1 or self.axes != 1:
-            _need_shape(positions, "positions", (self.axes, T))
-        if self.freqs.device != dev:
-            raise ValueError(f"the rotation's freqs are on {self.freqs.device}, expected {dev}")
+        self._device, self._freqs = freqs.device, freqs.data_ptr()
+
+    def _need_positions(self, positions: torch.Tensor, T: int, dev) -> int:
+        if self._device != dev:
+            raise ValueError(f"the rotation's freqs are on {self._device}, expected {dev}")
+        shape = (self.axes, T)
+        if self.axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1:
+            shape = (T,)
+        return _need_vector(positions, "positions", torch.int32, dev, shape)
 
 
 def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
@@ -759,22 +789,23 @@ def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
     x may be a slice (contiguous heads); out may be x itself.  inverse=True
     turns back, which is also the gradient of the forward call."""
     xv = _need_heads(x, "x", _FLOATS)
-    dev = x.device
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
-    T, H, D = x.shape
-    rope._need_positions(positions, T, dev)
+    dev, size = x.device, x.shape
+    T, H, D = size
+    pos = rope._need_positions(positions, T, dev)
     if out is None:
         dt = x.dtype if out_dtype is None else out_dtype
         if dt not in _TYPE_CODE:
             raise TypeError(f"out_dtype must be in {_FLOATS}")
-        out = torch.empty((T, H, D), dtype=dt, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
-    yv = _need_heads(out, "out", _FLOATS, dev)
-    _need_shape(out, "out", (T, H, D))
-    _launch(dev, "pq1_rope", load_library().pq1_rope, xv, yv, _ptr(positions), _ptr(rope.freqs),
-            rope._spec[bool(inverse)], T, H, D)
+        out = torch.empty(size, dtype=dt, device=dev)
+        yv = Pq1Heads(out.data_ptr(), _TYPE_CODE[dt], H * D, D)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
+        yv = _need_heads(out, "out", _FLOATS, dev, size)
+    _launch(dev, "pq1_rope", (_lib or load_library()).pq1_rope, xv, yv, pos, rope._freqs,
+            rope._spec[1 if inverse else 0], T, H, D)
     return out
 
 
@@ -790,6 +821,7 @@ class KVCache:
         _need_shape(v, "v", k.shape)
         self.k, self.v = k, v
         self.pages, self.heads, self.page_size, self.dim = (int(n) for n in k.shape)
+        self.dtype, self.device = k.dtype, k.device
         self._struct = Pq1KvCache(k.data_ptr(), v.data_ptr(), _TYPE_CODE[k.dtype],
                                   self.page_size, self.pages, self.heads, self.dim)
 
@@ -800,14 +832,6 @@ class KVCache:
         shape = (int(pages), int(heads), int(page_size), int(dim))
         return cls(torch.empty(shape, dtype=dtype, device=device),
                    torch.empty(shape, dtype=dtype, device=device))
-
-    @property
-    def dtype(self):
-        return self.k.dtype
-
-    @property
-    def device(self):
-        return self.k.device
 
 
 def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -820,37 +844,40 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
     type.  One launch."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
-    dev = cache.device
-    kv = _need_heads(k, "k", (torch.float32, cache.dtype), dev)
-    vv = _need_heads(v, "v", (k.dtype,), dev)
-    T = int(k.shape[0])
-    _need_shape(k, "k", (T, cache.heads, cache.dim))
-    _need_shape(v, "v", (T, cache.heads, cache.dim))
-    _need(slots, "slots", (torch.int64,), dev)
-    _need_shape(slots, "slots", (T,))
-    spec = None
+    dev, dt = cache.device, cache.dtype
+    kv = _need_heads(k, "k", (torch.float32, dt), dev)
+    T = k.shape[0]
+    shape = (T, cache.heads, cache.dim)
+    if k.shape != shape:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected {shape}")
+    kind = (k.dtype,)
+    vv = _need_heads(v, "v", kind, dev, shape)
+    at = _need_vector(slots, "slots", torch.int64, dev, (T,))
+    spec = pos = freqs = None
     if rope is not None:
         if not isinstance(rope, Rope):
             raise TypeError("rope must be a Rope")
         if positions is None:
             raise ValueError("a rotation needs positions")
-        rope._need_positions(positions, T, dev)
-        spec = rope._spec[0]
+        pos = rope._need_positions(positions, T, dev)
+        spec, freqs = rope._spec[0], rope._freqs
     qv = ov = None
     Hq = 0
     if q is not None:
-        qv = _need_heads(q, "q", (k.dtype,), dev)
-        Hq = int(q.shape[1])
-        _need_shape(q, "q", (T, Hq, cache.dim))
+        qv = _need_heads(q, "q", kind, dev)
+        size = q.shape
+        Hq = size[1]
+        if size[0] != T or size[2] != cache.dim:
+            raise ValueError(f"q has shape {tuple(size)}, expected {(T, Hq, cache.dim)}")
         if q_out is None:
-            q_out = torch.empty((T, Hq, cache.dim), dtype=cache.dtype, device=dev)
-        ov = _need_heads(q_out, "q_out", (cache.dtype,), dev)
-        _need_shape(q_out, "q_out", (T, Hq, cache.dim))
+            q_out = torch.empty(size, dtype=dt, device=dev)
+            ov = Pq1Heads(q_out.data_ptr(), _TYPE_CODE[dt], Hq * cache.dim, cache.dim)
+        else:
+            ov = _need_heads(q_out, "q_out", (dt,), dev, size)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _launch(dev, "pq1_kv_append", load_library().pq1_kv_append, kv, vv, _ptr(slots), qv, ov, Hq,
-            None if spec is None else _ptr(positions), None if spec is None else _ptr(rope.freqs),
-            spec, cache._struct, T)
+    _launch(dev, "pq1_kv_append", (_lib or load_library()).pq1_kv_append, kv, vv, at, qv, ov, Hq,
+            pos, freqs, spec, cache._struct, T)
     return q_out
 
 
@@ -860,7 +887,7 @@ _attn_ws = {}
 
 
 def attention_workspace(need: int, device: torch.device) -> torch.Tensor:
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    key = (device.index, _raw_stream(device.index))
     with _ws_lock:
         ws = _attn_ws.get(key)
         if ws is None or ws.numel() < need:
@@ -886,33 +913,37 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
     given; rows that no sequence owns keep what they held."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
-    dev = cache.device
-    qv = _need_heads(q, "q", (cache.dtype,), dev)
-    T, Hq, D = (int(n) for n in q.shape)
-    _need_shape(q, "q", (T, Hq, cache.dim))
-    _need(page_table, "page_table", (torch.int32,), dev)
+    dev, dt = cache.device, cache.dtype
+    qv = _need_heads(q, "q", (dt,), dev)
+    size = q.shape
+    T, Hq, D = size
+    if D != cache.dim:
+        raise ValueError(f"q has shape {tuple(size)}, expected {(T, Hq, cache.dim)}")
+    if not isinstance(page_table, torch.Tensor):
+        raise TypeError("page_table must be a torch.Tensor")
     if page_table.dim() != 2:
         raise ValueError("page_table must be 2-D, [sequences][pages]")
-    B, max_pages = (int(n) for n in page_table.shape)
-    _need(cu_q, "cu_q", (torch.int32,), dev)
-    _need_shape(cu_q, "cu_q", (B + 1,))
-    _need(kv_len, "kv_len", (torch.int32,), dev)
-    _need_shape(kv_len, "kv_len", (B,))
+    B, max_pages = page_table.shape
+    table = _need_vector(page_table, "page_table", torch.int32, dev, (B, max_pages))
+    cu = _need_vector(cu_q, "cu_q", torch.int32, dev, (B + 1,))
+    lens = _need_vector(kv_len, "kv_len", torch.int32, dev, (B,))
     if out is None:
-        dt = cache.dtype if out_dtype is None else out_dtype
-        if dt not in (cache.dtype, torch.float32):
-            raise TypeError(f"out_dtype must be {cache.dtype} or torch.float32")
-        out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
-    ov = _need_heads(out, "out", (cache.dtype, torch.float32), dev)
-    _need_shape(out, "out", (T, Hq, D))
-    lib = load_library()
+        if out_dtype is not None:
+            if out_dtype != dt and out_dtype != torch.float32:
+                raise TypeError(f"out_dtype must be {dt} or torch.float32")
+            dt = out_dtype
+        out = torch.empty(size, dtype=dt, device=dev)
+        ov = Pq1Heads(out.data_ptr(), _TYPE_CODE[dt], Hq * D, D)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
+        ov = _need_heads(out, "out", (dt, torch.float32), dev, size)
+    lib = _lib or load_library()
     max_q, max_kv = int(max_q), int(max_kv)
     need = lib.pq1_paged_attention_workspace_bytes(B, T, Hq, cache.heads, D, max_q, max_kv)
-    ws = attention_workspace(need, dev) if need else None
-    _launch(dev, "pq1_paged_attention", lib.pq1_paged_attention, qv, ov, cache._struct,
-            _ptr(page_table), max_pages, _ptr(cu_q), _ptr(kv_len), B, T, Hq, max_q, max_kv,
-            D ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window),
-            _ptr(ws), need)
+    ws = attention_workspace(need, dev).data_ptr() if need else None
+    _launch(dev, "pq1_paged_attention", lib.pq1_paged_attention, qv, ov, cache._struct, table,
+            max_pages, cu, lens, B, T, Hq, max_q, max_kv,
+            D ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window), ws,
+            need)
     return out
