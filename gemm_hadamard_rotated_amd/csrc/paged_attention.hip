@@ -449,9 +449,11 @@ hipError_t launch_join(const AttnPlan& plan, const AttnArgs& a, void* workspace,
   const float* part_o = static_cast<const float*>(workspace);
   const float2* part_ml = reinterpret_cast<const float2*>(
       part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
-  const dim3 grid(static_cast<uint32_t>(a.B * plan.tokens * ((a.Hk * a.G + 3) / 4)));
-  join_kernel<TO, D><<<grid, 256, 0, s>>>(a, fg, plan.tile_rows, static_cast<int>(plan.tokens),
-                                          part_o, part_ml);
+  const int64_t heads4 = (a.Hk * a.G + 3) / 4;
+  const int64_t most = ((int64_t{1} << 24) - 1) / (a.B * heads4);  // below 2^32 threads
+  const int64_t tokens = plan.tokens < most ? plan.tokens : most;
+  join_kernel<TO, D><<<dim3(static_cast<uint32_t>(a.B * tokens * heads4)), 256, 0, s>>>(
+      a, fg, plan.tile_rows, static_cast<int>(tokens), part_o, part_ml);
   return hipGetLastError();
 }
 
@@ -487,26 +489,38 @@ constexpr int64_t kFewRows = 64;
 
 AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_q,
                         int64_t max_kv) {
+  // A launch holds less than 2^32 threads.  Kernels walk on over rows that
+  // their grid has no workgroup for, so a long chunk only costs balance.
+  constexpr int64_t most = (int64_t{1} << 32) / (2 * kTileRows) - 1;
+  constexpr int64_t cus = 256;
   AttnPlan p;
+  if (B * Hk > most) return p;
+  p.fits = true;
   p.tokens = max_q < 1 ? 1 : max_q < T ? max_q : T;
   const int64_t rows = p.tokens * (Hq / Hk);
   p.many = rows > kFewRows;
   p.tile_rows = p.many ? kTileRows : rows <= 16 ? 16 : 32;
   p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  // Parts: enough workgroups for two on each of the 256 CUs, but no part
-  // shorter than one key tile for each wave.
+  if (p.row_tiles > most / (B * Hk)) p.row_tiles = most / (B * Hk);
   const int64_t kv = max_kv < 1 ? 1 : max_kv > 0x7fffffff ? 0x7fffffff : max_kv;
   const int64_t units = B * Hk * p.row_tiles;
   const int64_t step = kKeys * kWaves;
-  int64_t chunk = (kv * units / 512 + step - 1) / step * step;
-  if (units >= 512 || chunk > kv) chunk = (kv + step - 1) / step * step;
-  if (chunk < step) chunk = step;
+  int64_t parts = 1;
+  if (p.many) {
+    // One workgroup to a CU: as many parts as the device takes at once.  More,
+    // to even out a last round, cost more than they give (192 workgroups of
+    // 7168 keys: 396 us; in 4 parts, three full rounds: 407 us and 48 to join
+    // them): idle CUs leave the others a higher clock.
+    while (units * (parts + 1) <= cus && (parts + 1) * 256 <= kv) ++parts;
+  } else if (units < 2 * cus) {
+    // Enough workgroups for two on each CU, but no part shorter than one key
+    // tile for each wave.
+    parts = (2 * cus + units - 1) / units;
+  }
+  int64_t chunk = ((kv + parts - 1) / parts + step - 1) / step * step;
   p.chunk = chunk > 0x7fffff00 ? 0x7fffff00 : static_cast<int>(chunk);
   p.nsplit = static_cast<int>((kv + p.chunk - 1) / p.chunk);
   p.workspace_bytes = p.nsplit > 1 ? static_cast<size_t>(p.nsplit) * T * Hq * (D * 4 + 8) : 0;
-  const int64_t most = 0x7fffffff;
-  p.fits = B <= most / Hk && B * Hk <= most / p.row_tiles && units <= most / p.nsplit &&
-           B <= most / Hq && B * Hq <= most / p.tokens;
   return p;
 }
 

@@ -1,26 +1,33 @@
 // Attention over a paged cache for many rows: prompts and chunks of prompts.
 //
-// A workgroup takes 32 RB rows for each of its waves, of one (sequence, cache
-// head), and walks tiles of 64 keys.  A tile's K and V rows are copied one
-// tile ahead straight from the cache into LDS (a lane gives the address of
-// its 16 bytes, so a tile's pages may lie anywhere); every wave reads them all.
+// A workgroup takes 256 rows of one (sequence, cache head), 32 for each of its
+// eight waves, and walks tiles of keys (64; 32 where D is 256).  A tile's K
+// and V rows are copied two tiles ahead straight from the cache into LDS (a
+// lane gives the address of its 16 bytes, so a tile's pages may lie anywhere);
+// every wave reads them all.
 //
 // Both products are taken transposed on 32x32x16 matrix instructions:
 // S^T = K Q^T leaves lane l the scores of row l % 32 for keys 8 (i / 4) + 4 g
 // + i % 4 (g = l / 32, i < 16), and eight of these are, as they stand, an
 // operand of O^T = V^T P^T if V is read with the same key order, which LDS
-// reads that transpose 4 keys x 16 dimensions do.  So P never leaves its lane, and a row's
-// maximum and sum need one exchange between the two halves of a wave.
+// reads that transpose 4 keys x 16 dimensions do.  So P never leaves its lane,
+// and a row's maximum and sum need one exchange between the halves of a wave.
 //
-// 16-byte pieces of a row are stored XORed with bits of the row number, so
-// that the rows read together lie in distinct banks (k_bits, v_bits).
+// Bound: the matrix instructions.  8192 rows of 8 cache heads against 7168
+// keys take 471 us at D = 256 (1021 TFLOP/s), 282 us at 128 (850) and 198 us at
+// 64 (609); a large library product reaches 1263 TFLOP/s on the same card, and
+// this loop with its reads, copies and softmax taken out 1366 at D = 256.
+// What was measured on the way: the scores and outputs of a wave fill its
+// registers (two waves a SIMD; 64 rows a wave spills, one wave a SIMD of 64
+// rows is slower, 759 against 505 us for 2048 tokens after 6144 at D = 256);
+// page numbers from LDS and no other load in the loop, so that copies stay in
+// flight over the barrier (478 -> 458 us); waves of one SIMD set half a tile
+// apart: no gain (the compiler's own order overlaps them as well).
 #include "attn_tiles.h"
 
 namespace pq1 {
 
 namespace {
-
-constexpr int kTileKeys = 64;
 
 using F16 = __attribute__((ext_vector_type(16))) float;
 using S4 = __attribute__((ext_vector_type(4))) short;
@@ -58,24 +65,48 @@ __device__ __forceinline__ int here(int x) {
   return x;
 }
 
+// Copies 16 bytes a lane from memory to LDS, lane after lane from `to` on (the
+// same for the whole wave).  Written as an instruction because the compiler
+// would wait for all copies in flight before each read of LDS that it cannot
+// tell apart from them; here the wait is wait_copies and a barrier.
+__device__ __forceinline__ void copy16(const char* from, char* to) {
+  const uint32_t at = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)to));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(from)
+               : "m0");
+}
+// Waits until at most N copies of this wave are in flight.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+constexpr int kPages = 4096;  // page numbers kept in LDS
+
 struct TileGrid {
   int row_tiles, nsplit, chunk;
 };
 
-template <typename T, typename TO, int D, int NW, int RB>
-__global__ __launch_bounds__(64 * NW) void many_rows_kernel(AttnArgs a, TileGrid tg,
-                                                            float* part_o, float2* part_ml) {
+constexpr int kTileWaves = kTileRows / 32;
+
+template <typename T, typename TO, int D>
+__global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, TileGrid tg,
+                                                                    float* part_o,
+                                                                    float2* part_ml) {
   constexpr int NP = kParts<T, TO>;
+  constexpr int KT = D == 256 ? 32 : 64;        // keys of a tile
   constexpr int ROWB = 2 * D;                   // bytes of a cache row
-  constexpr int TILE = kTileKeys * ROWB;
+  constexpr int TILE = KT * ROWB;
   constexpr int PIECES = D / 8;                 // 16-byte pieces of a row
   constexpr int CROWS = 64 / PIECES;            // rows one copy of a wave fills
-  constexpr int COPIES = kTileKeys / (CROWS * NW);
-  constexpr int ROWS = 32 * RB * NW;
+  constexpr int COPIES = KT / (CROWS * kTileWaves);
   constexpr int NB = D / 32;                    // blocks of 32 dimensions
-  constexpr int EB = D * RB >= 256 ? 1 : 2;     // blocks of 32 keys whose scores are held
-  __shared__ __attribute__((aligned(1024))) char k0_lds[TILE], v0_lds[TILE];
-  __shared__ __attribute__((aligned(1024))) char k1_lds[TILE], v1_lds[TILE];
+  constexpr int EB = KT / 32;                   // blocks of 32 keys
+  constexpr int AHEAD = D == 256 ? 3 : 4;       // fragments in flight from LDS
+  __shared__ __attribute__((aligned(TILE))) char k_lds[3 * TILE], v_lds[3 * TILE];
+  __shared__ int32_t page_lds[kPages + 1];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -95,278 +126,301 @@ __global__ __launch_bounds__(64 * NW) void many_rows_kernel(AttnArgs a, TileGrid
   const int Hq = a.Hk * a.G;
   const int page_mask = (1 << a.page_shift) - 1;
 
-  for (int64_t r0 = static_cast<int64_t>(rt) * ROWS; r0 < rows;
-       r0 += static_cast<int64_t>(tg.row_tiles) * ROWS) {
-    const Parts pt = split_keys(a, s, static_cast<int>(r0), ROWS, tg.chunk, tg.nsplit);
+  for (int64_t r0 = static_cast<int64_t>(rt) * kTileRows; r0 < rows;
+       r0 += static_cast<int64_t>(tg.row_tiles) * kTileRows) {
+    const Parts pt = split_keys(a, s, static_cast<int>(r0), kTileRows, tg.chunk, tg.nsplit);
     if (split > 0 && split >= pt.count) continue;
     const int k0 = pt.start + split * pt.chunk;
     const int k1 = pt.hi - k0 < pt.chunk ? pt.hi : k0 + pt.chunk;
 
     // this wave's rows, and the keys that some of them sees
-    const int wr0 = static_cast<int>(r0) + 32 * RB * wave;
+    const int wr0 = static_cast<int>(r0) + 32 * wave;
     int wlo = 0, whi = 0;
     if (wr0 < rows) {
       int t;
-      const int last = (wr0 + 32 * RB < rows ? wr0 + 32 * RB : rows) - 1;
+      const int last = (wr0 + 32 < rows ? wr0 + 32 : rows) - 1;
       visible(a, s, wr0 / a.G, &wlo, &t);
       visible(a, s, last / a.G, &t, &whi);
     }
-    int hi[RB];  // row col of a block sees keys [low(hi), hi)
-    const auto low = [&](int end) { return a.window > 0 && end > a.window ? end - a.window : 0; };
-    U4 q[RB][D / 16];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const int r = wr0 + 32 * rb + col;
-      hi[rb] = 0;
+    U4 q[D / 16];
+    {
+      const int r = wr0 + col;
       const int i = r / a.G;
-      int t;
-      if (r < rows) visible(a, s, i, &t, &hi[rb]);
       const T* src = static_cast<const T*>(a.q) + (s.q0 + i) * a.q_ts +
                      (h * a.G + r - i * a.G) * a.q_hs + 8 * g;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d)
-        q[rb][d] = r < rows ? *reinterpret_cast<const U4*>(src + 16 * d) : U4{0, 0, 0, 0};
+        q[d] = r < rows ? *reinterpret_cast<const U4*>(src + 16 * d) : U4{0, 0, 0, 0};
     }
-    F16 o[RB][NB];
-    float m[RB], l[RB];
+    F16 o[NB];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      m[rb] = kNegInf;
-      l[rb] = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NB; ++n) o[rb][n] = F16{};
-    }
-
+    for (int n = 0; n < NB; ++n) o[n] = F16{};
+    float m = kNegInf, l = 0.0f;
     bool odd_values = false;  // infinities or NaN were taken out of V
 
-    // Page of key j0 + lane; keys past the last take its page, so that every
-    // address lies in the cache.  -1: no page of the cache.
-    auto find_page = [&](int j0) {
-      const int j = j0 + lane < pt.hi ? j0 + lane : pt.hi - 1;
-      const int p = j >> a.page_shift;
-      const int page = p < a.max_pages ? table[p] : -1;
-      return page < 0 || page >= a.pages ? -1 : page;
+    // Pages of keys first .. end - 1 are in LDS; -1: no page of the cache.
+    // Keys past the last take its page, so that every address lies in the
+    // cache.  A lane looks up the rows that it copies, a tile ahead.
+    int first = 0, end = 0;
+    auto page_at = [&](int j) { return page_lds[(j >> a.page_shift) - (first >> a.page_shift)]; };
+    auto up_to_end = [&](int j) { return j < end ? j : end - 1; };
+    auto gone_of = [&](int j0) {  // keys of a tile on no page of the cache
+      const uint64_t bits = __ballot(page_at(up_to_end(j0 + lane)) < 0);
+      return KT == 64 ? bits : bits & 0xffffffffu;
     };
     auto row_of = [&](int page, int j) {
       return ((static_cast<int64_t>(page < 0 ? 0 : page) * a.Hk + h) << a.page_shift) +
              (j & page_mask);
     };
-    auto copy = [&](int page, int j0, char* kb, char* vb) {
-      const int j = j0 + lane < pt.hi ? j0 + lane : pt.hi - 1;
-      const int64_t mine = row_of(page, j) * ROWB;
-      const int mlo = static_cast<int>(mine), mhi = static_cast<int>(mine >> 32);
-      const int ln = here(lane);
-      const int r = wave * (COPIES * CROWS) + ln / PIECES;  // the row of copy 0
-      const int kp = 16 * (ln % PIECES ^ k_bits<D>(r)), vp = 16 * (ln % PIECES ^ v_bits<D>(r));
+    const int crow = wave * (COPIES * CROWS) + lane / PIECES;  // the row of copy 0
+    auto find_pages = [&](int j0, int (&page)[COPIES]) {
+#pragma unroll
+      for (int c = 0; c < COPIES; ++c) page[c] = page_at(up_to_end(j0 + crow + c * CROWS));
+    };
+    auto copy = [&](const int (&page)[COPIES], int j0, char* kb, char* vb) {
+      const int r = here(crow), piece = here(lane) % PIECES;
+      const int kp = 16 * (piece ^ k_bits<D>(r)), vp = 16 * (piece ^ v_bits<D>(r));
 #pragma unroll
       for (int c = 0; c < COPIES; ++c) {
-        const int64_t at = (static_cast<int64_t>(__shfl(mhi, r + c * CROWS)) << 32) |
-                           static_cast<uint32_t>(__shfl(mlo, r + c * CROWS));
+        const int64_t at = row_of(page[c], up_to_end(j0 + r + c * CROWS)) * ROWB;
         const int to = (wave * COPIES + c) * 1024;
-        __builtin_amdgcn_global_load_lds(
-            (GlobalVoid*)(static_cast<const char*>(a.k_cache) + at +
-                          (kp ^ 16 * k_bits<D>(c * CROWS))),
-            (LdsVoid*)(kb + to), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(
-            (GlobalVoid*)(static_cast<const char*>(a.v_cache) + at +
-                          (vp ^ 16 * v_bits<D>(c * CROWS))),
-            (LdsVoid*)(vb + to), 16, 0, 0);
+        copy16(static_cast<const char*>(a.k_cache) + at + (kp ^ 16 * k_bits<D>(c * CROWS)),
+               kb + to);
+        copy16(static_cast<const char*>(a.v_cache) + at + (vp ^ 16 * v_bits<D>(c * CROWS)),
+               vb + to);
       }
     };
+    // A tile that not every row sees whole, or with a page missing
+    auto is_edge = [&](int j0, uint64_t gone) {
+      return j0 < pt.lo_max || j0 + KT > pt.hi_min || gone != 0;
+    };
+    // Values no row sees become zero, and where there are infinities or NaN
+    // among the others these too: times a probability of zero they would be
+    // NaN in the rows that do not see them.
+    auto clean = [&](char* vb, int j0, uint64_t gone) {
+      bool odd = false;
+#pragma unroll
+      for (int e = 0; e < TILE / 16 / (64 * kTileWaves); ++e) {
+        const int at = 64 * kTileWaves * e + here(threadIdx.x);
+        const int r = at / PIECES;
+        U4* v = reinterpret_cast<U4*>(vb + 16 * at);
+        U4 x = *v;
+        const bool seen = j0 + r >= pt.lo && j0 + r < pt.hi && !(gone >> r & 1);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          x[w] = seen ? x[w] : 0u;
+          odd |= not_finite<T>(x[w]);
+          x[w] = finite_or_zero<T>(x[w]);
+        }
+        *v = x;
+      }
+      odd_values |= __syncthreads_or(odd) != 0;
+    };
 
+    const int kat = col * ROWB + 16 * (g ^ k_bits<D>(col));
     const int vrow = 4 * g + ((lane & 15) >> 2);           // V row of a transposing read
     const int vpiece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const int kat = col * ROWB + 16 * (g ^ k_bits<D>(col));
     const int vat = vrow * ROWB + 16 * (vpiece ^ v_bits<D>(vrow)) + 8 * (lane & 1);
 
-    auto tile = [&](const char* kb, char* vb, int j0, int page) {
-      const uint64_t gone = __ballot(page < 0);  // keys on no page of the cache
-      const bool edge = j0 < pt.lo_max || j0 + kTileKeys > pt.hi_min || gone != 0;
-      if (edge) {
-        // Values no row sees become zero, and where there are infinities or
-        // NaN among the others these too: times a probability of zero they
-        // would be NaN in the rows that do not see them.
-        bool odd = false;
-        constexpr int EACH = TILE / 16 / (64 * NW);
+    // S^T = K Q^T.  Fragments are read AHEAD steps before their products; steps
+    // that share an address but for a constant follow one another.
+    auto scores = [&](const char* kb, F16 (&sc)[EB]) {
+      const auto step = [](int n) {
+        return D == 256 ? n / 2 + 8 * (n % 2) : n / EB;
+      };
+      const int kx = here(kat);
+      U4 kf[AHEAD];
+      auto read = [&](int n) {
+        const int e = EB == 2 ? n % 2 : 0, d = step(n);
+        return *reinterpret_cast<const U4*>(kb + 32 * e * ROWB + (kx ^ 32 * (d & 7)) +
+                                            256 * (d >> 3));
+      };
+      constexpr int N = EB * D / 16;
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-          const int at = 64 * NW * e + here(threadIdx.x);
-          const int r = at / PIECES;
-          U4* v = reinterpret_cast<U4*>(vb + 16 * at);
-          U4 x = *v;
-          const bool seen = j0 + r >= pt.lo && j0 + r < pt.hi && !(gone >> r & 1);
+      for (int n = 0; n < AHEAD; ++n) kf[n] = read(n);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            x[w] = seen ? x[w] : 0u;
-            odd |= not_finite<T>(x[w]);
-            x[w] = finite_or_zero<T>(x[w]);
-          }
-          *v = x;
-        }
-        odd_values |= __syncthreads_or(odd) != 0;
+      for (int n = 0; n < N; ++n) {
+        const int e = EB == 2 ? n % 2 : 0;
+        sc[e] = mfma32(kf[n % AHEAD], q[step(n)], n < EB ? F16{} : sc[e], T{});
+        if (n + AHEAD < N) kf[n % AHEAD] = read(n + AHEAD);
       }
-      if (j0 >= whi || j0 + kTileKeys <= wlo) return;  // this wave's rows see none of it
-
+      __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
 #pragma unroll
-      for (int e0 = 0; e0 < 2; e0 += EB) {
-        const int kx = here(kat), vx = here(vat);
-        F16 sc[RB][EB];
-#pragma unroll
-        for (int e = 0; e < EB; ++e)
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            const U4 f = *reinterpret_cast<const U4*>(
-                kb + 32 * (e0 + e) * ROWB + (kx ^ 32 * (d & 7)) + 256 * (d >> 3));
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-              sc[rb][e] = mfma32(f, q[rb][d], d == 0 ? F16{} : sc[rb][e], T{});
-          }
-        if (edge) {
-          // key numbers relative to the lane's first: compile-time constants
-          const int at = j0 + 32 * e0 + 4 * g;
-          const uint64_t lost = gone >> (32 * e0 + 4 * g);
-#pragma unroll
-          for (int e = 0; e < EB; ++e)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int key = 32 * e + 8 * (i >> 2) + (i & 3);
-#pragma unroll
-              for (int rb = 0; rb < RB; ++rb) {
-                const bool seen = key >= low(hi[rb]) - at && key < hi[rb] - at;
-                sc[rb][e][i] =
-                    !seen ? kNegInf : lost >> key & 1 ? __builtin_nanf("") : sc[rb][e][i];
-              }
-            }
-        }
-        U4 pr[RB][EB][2][NP];
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          float top = sc[rb][0][0];
-#pragma unroll
-          for (int e = 0; e < EB; ++e)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[rb][e][i]);
-          const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(top),
-                                                           __float_as_uint(top), false, false);
-          top = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])) * a.scale_log2;
-          if (__any(top > m[rb] + kLag)) {
-            const float up = fmaxf(m[rb], top);
-            const float keep = m[rb] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[rb] - up);
-            m[rb] = up;
-            l[rb] *= keep;
-#pragma unroll
-            for (int n = 0; n < NB; ++n) o[rb][n] *= keep;
-          }
-          const float shift = m[rb] == kNegInf ? 0.0f : kUp - m[rb];
-#pragma unroll
-          for (int e = 0; e < EB; ++e)
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              float p[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(fmaf(sc[rb][e][8 * st + i], a.scale_log2, shift));
-                l[rb] += p[i];
-              }
-              split_probs<T, NP>(p, pr[rb][e][st]);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < EB; ++e)
-#pragma unroll
-          for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-              const char* src = vb + (32 * (e0 + e) + 16 * st) * ROWB + (vx ^ 64 * (n & 3)) +
-                                256 * (n >> 2);
-              const U2 x = __builtin_bit_cast(
-                  U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4*)src));
-              const U2 y = __builtin_bit_cast(
-                  U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4*)(src + 8 * ROWB)));
-              const U4 f = {x[0], x[1], y[0], y[1]};
-#pragma unroll
-              for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-                for (int z = NP - 1; z >= 0; --z)
-                  o[rb][n] = mfma32(f, pr[rb][e][st][z], o[rb][n], T{});
-            }
-        if (e0 + EB < 2) __builtin_amdgcn_sched_barrier(0);
+      for (int n = 0; n < N; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (n + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
     };
 
-    // Tile t is computed while t + 1 is copied into the other buffers; a wave
-    // waits for its own copies before the barrier that ends a tile.
-    if (k0 < k1) {
-      int page = find_page(k0);
-      copy(page, k0, k0_lds, v0_lds);
-      int next = find_page(k0 + kTileKeys);
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vector memory 0
-      __syncthreads();
-      for (int j0 = k0;;) {
-        if (j0 + kTileKeys < k1) copy(next, j0 + kTileKeys, k1_lds, v1_lds);
-        int then = find_page(j0 + 2 * kTileKeys);
-        tile(k0_lds, v0_lds, j0, page);
-        __builtin_amdgcn_s_waitcnt(0x0F70);
-        __syncthreads();
-        page = next;
-        next = then;
-        if ((j0 += kTileKeys) >= k1) break;
-        if (j0 + kTileKeys < k1) copy(next, j0 + kTileKeys, k0_lds, v0_lds);
-        then = find_page(j0 + 2 * kTileKeys);
-        tile(k1_lds, v1_lds, j0, page);
-        __builtin_amdgcn_s_waitcnt(0x0F70);
-        __syncthreads();
-        page = next;
-        next = then;
-        if ((j0 += kTileKeys) >= k1) break;
+    // Softmax of the scores, O^T += V^T P^T.
+    auto products = [&](const char* vb, int j0, uint64_t gone, F16 (&sc)[EB]) {
+      if (is_edge(j0, gone)) {
+        // key numbers relative to the lane's first: compile-time constants
+        const int at = j0 + 4 * g;
+        const uint64_t lost = gone >> (4 * g);
+        int lo = 0, hi = 0;
+        const int r = wr0 + here(lane) % 32;
+        if (r < rows) visible(a, s, r / a.G, &lo, &hi);
+        lo -= at;
+        hi -= at;
+#pragma unroll
+        for (int e = 0; e < EB; ++e)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = 32 * e + 8 * (i >> 2) + (i & 3);
+            sc[e][i] = key < lo || key >= hi    ? kNegInf
+                       : (lost >> key & 1) != 0 ? __builtin_nanf("")
+                                                : sc[e][i];
+          }
       }
+      float top = sc[0][0];
+#pragma unroll
+      for (int e = 0; e < EB; ++e)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[e][i]);
+      const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top),
+                                                       false, false);
+      top = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])) * a.scale_log2;
+      if (__any(top > m + kLag)) {
+        const float up = fmaxf(m, top);
+        const float keep = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - up);
+        m = up;
+        l *= keep;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) o[n] *= keep;
+      }
+      const float shift = m == kNegInf ? 0.0f : kUp - m;
+      U4 pr[2 * EB][NP];
+#pragma unroll
+      for (int st = 0; st < 2 * EB; ++st) {
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(fmaf(sc[st / 2][8 * (st % 2) + i], a.scale_log2, shift));
+          l += p[i];
+        }
+        split_probs<T, NP>(p, pr[st]);
+      }
+      const int vx = here(vat);
+      U4 vf[AHEAD];
+      auto read = [&](int n) {
+        const int d = n % NB;
+        const char* src = vb + 16 * (n / NB) * ROWB + (vx ^ 64 * (d & 3)) + 256 * (d >> 2);
+        const U2 x = __builtin_bit_cast(
+            U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4*)src));
+        const U2 y = __builtin_bit_cast(
+            U2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4*)(src + 8 * ROWB)));
+        return U4{x[0], x[1], y[0], y[1]};
+      };
+      constexpr int N = 2 * EB * NB;
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) vf[n] = read(n);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int z = NP - 1; z >= 0; --z)
+          o[n % NB] = mfma32(vf[n % AHEAD], pr[n / NB][z], o[n % NB], T{});
+        if (n + AHEAD < N) vf[n % AHEAD] = read(n + AHEAD);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 1);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x008, NP, 1);
+        if (n + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
+      }
+    };
+
+    // Tile t is computed while t + 2 is copied (past the last tile, its last
+    // key again); before the barrier that ends a tile a wave waits until only
+    // that copy is in flight, so its part of the next tile is complete.  The
+    // page numbers come from LDS, as many as fit at a time: with no other load
+    // in the loop, the count of copies in flight is known.
+    for (first = k0; first < k1; first = end) {
+      const int64_t most = static_cast<int64_t>(first) + (int64_t{kPages - 1} << a.page_shift);
+      end = k1 < most ? k1 : static_cast<int>(most - (most - first) % KT);
+      const int p0 = first >> a.page_shift, p1 = (end - 1) >> a.page_shift;
+      bool lost = false;
+      __syncthreads();  // the last tile of the keys before is done
+      for (int p = p0 + static_cast<int>(threadIdx.x); p <= p1; p += 64 * kTileWaves) {
+        const int page = p < a.max_pages ? table[p] : -1;
+        const bool bad = page < 0 || page >= a.pages;
+        page_lds[p - p0] = bad ? -1 : page;
+        lost |= bad;
+      }
+      const bool any_gone = __syncthreads_or(lost);
+      int page[COPIES];
+      find_pages(first, page);
+      copy(page, first, k_lds, v_lds);
+      find_pages(first + KT, page);
+      copy(page, first + KT, k_lds + TILE, v_lds + TILE);
+      find_pages(first + 2 * KT, page);
+      wait_copies<2 * COPIES>();
+      __syncthreads();
+      int now = 0, then = 2 * TILE;
+#pragma unroll 1
+      for (int j0 = first; j0 < end; j0 += KT) {
+        const uint64_t gone = any_gone ? gone_of(j0) : 0;
+        if (is_edge(j0, gone)) clean(v_lds + now, j0, gone);
+        copy(page, j0 + 2 * KT, k_lds + then, v_lds + then);
+        find_pages(j0 + 3 * KT, page);
+        F16 sc[EB];
+        scores(k_lds + now, sc);
+        products(v_lds + now, j0, gone, sc);
+        wait_copies<2 * COPIES>();
+        __syncthreads();
+        now = now == 2 * TILE ? 0 : now + TILE;
+        then = then == 2 * TILE ? 0 : then + TILE;
+      }
+      wait_copies<0>();
     }
 
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[rb]),
-                                                       __float_as_uint(l[rb]), false, false);
+    {
+      const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l),
+                                                       false, false);
       const float sum = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
-      const int r = wr0 + 32 * rb + col;
-      if (r >= rows) continue;
-      const int i = r / a.G;
-      const int hq = h * a.G + r - i * a.G;
-      const int64_t at_row = static_cast<int64_t>(split) * a.T * Hq + (s.q0 + i) * Hq + hq;
-      if (tg.nsplit > 1) {
-        if (g == 0) part_ml[at_row] = make_float2(m[rb], sum);
-      }
-      const float inv = 1.0f / sum;
+      const int r = wr0 + col;
+      if (r < rows) {
+        const int i = r / a.G;
+        const int hq = h * a.G + r - i * a.G;
+        const int64_t at_row = static_cast<int64_t>(split) * a.T * Hq + (s.q0 + i) * Hq + hq;
+        if (tg.nsplit > 1 && g == 0) part_ml[at_row] = make_float2(m, sum);
+        const float inv = 1.0f / sum;
+        int lo, hi;
+        visible(a, s, i, &lo, &hi);
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-          const int d = 32 * n + 8 * i4 + 4 * g;
-          float y[4];
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const int d = 32 * n + 8 * i4 + 4 * g;
+            float y[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) y[c] = o[rb][n][4 * i4 + c];
-          if (tg.nsplit > 1) {
-            store_wide(part_o + at_row * D + d, y);
-          } else {
+            for (int c = 0; c < 4; ++c) y[c] = o[n][4 * i4 + c];
+            if (tg.nsplit > 1) {
+              store_wide(part_o + at_row * D + d, y);
+            } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = hi[rb] > 0 ? y[c] * inv : 0.0f;
-            store_wide(static_cast<TO*>(a.out) + (s.q0 + i) * a.o_ts + hq * a.o_hs + d, y);
+              for (int c = 0; c < 4; ++c) y[c] = hi > lo ? y[c] * inv : 0.0f;
+              store_wide(static_cast<TO*>(a.out) + (s.q0 + i) * a.o_ts + hq * a.o_hs + d, y);
+            }
           }
-        }
+      }
     }
 
     // Put back what the tiles' edges took out: rows that see an infinity or
     // NaN add it to their result.
     if (odd_values) {
       __syncthreads();
-      for (int j0 = k0; j0 < k1; j0 += kTileKeys) {
-        const int page = find_page(j0);
-        const bool bad = __any(page < 0);
-        if (j0 >= pt.lo_max && j0 + kTileKeys <= pt.hi_min && !bad) continue;
-        for (int key = 0; key < kTileKeys && j0 + key < k1; ++key) {
+      for (int j0 = k0; j0 < k1; j0 += KT) {
+        const int j = j0 + lane < k1 ? j0 + lane : k1 - 1;
+        const int p = j >> a.page_shift;
+        int page = p < a.max_pages ? table[p] : -1;
+        if (page >= a.pages) page = -1;
+        if (!is_edge(j0, __any(page < 0))) continue;
+        for (int key = 0; key < KT && j0 + key < k1; ++key) {
           const int pg = __shfl(page, key);
           if (pg < 0) continue;
           const T* src = static_cast<const T*>(a.v_cache) + row_of(pg, j0 + key) * D;
-          for (int e = threadIdx.x; e < ROWS * D; e += 64 * NW) {
+          for (int e = threadIdx.x; e < kTileRows * D; e += 64 * kTileWaves) {
             const int64_t r = r0 + e / D;
             const int d = e % D;
             const float x = static_cast<float>(src[d]);
@@ -386,6 +440,7 @@ __global__ __launch_bounds__(64 * NW) void many_rows_kernel(AttnArgs a, TileGrid
         }
       }
     }
+    __syncthreads();  // the next tile of rows takes the buffers
   }
 }
 
@@ -396,8 +451,7 @@ hipError_t launch_tiles(const AttnPlan& plan, const AttnArgs& a, void* workspace
   float2* part_ml =
       reinterpret_cast<float2*>(part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
   const dim3 grid(static_cast<uint32_t>(a.B * a.Hk * plan.row_tiles * plan.nsplit));
-  constexpr int RB = 1, NW = kTileRows / (32 * RB);
-  many_rows_kernel<T, TO, D, NW, RB><<<grid, 64 * NW, 0, s>>>(a, tg, part_o, part_ml);
+  many_rows_kernel<T, TO, D><<<grid, 64 * kTileWaves, 0, s>>>(a, tg, part_o, part_ml);
   return hipGetLastError();
 }
 
