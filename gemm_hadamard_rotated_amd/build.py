@@ -50,6 +50,7 @@ BENCH_SOURCES = ["bench_kernels.hip"]
 # reads them right away; the accumulator-register form cost a copy each).
 # paged_attention_tiles.hip: likewise, scores and outputs are read by the softmax.
 SOURCE_FLAGS: dict = {"gemm_skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+                      "paged_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
                       "paged_attention_tiles.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 HIPCC_FLAGS = [

@@ -16,6 +16,7 @@ using pq1::overlaps;
 
 constexpr int kMaxHeads = 1024, kMaxDim = 1024;
 constexpr int64_t kMaxTokens = int64_t{1} << 30;
+constexpr int64_t kMaxRows = 0x7ff00000;  // of T * Hq: row numbers plus a tile stay in 31 bits
 constexpr int64_t kMaxElems = int64_t{1} << 38;   // of one call's views
 constexpr int64_t kMaxStride = int64_t{1} << 31;  // elements
 
@@ -127,7 +128,7 @@ pq1_status check_attention_sizes(int64_t B, int64_t T, int64_t Hq, int64_t heads
   if (heads < 1 || heads > kMaxHeads || Hq < heads || Hq > kMaxHeads || Hq % heads != 0)
     return PQ1_ERR_SHAPE;
   if (B < 0 || T < 0 || max_q < 0 || max_kv < 0) return PQ1_ERR_SHAPE;
-  if (T >= kMaxTokens || T * Hq > 0x7fffffff || B >= kMaxTokens) return PQ1_ERR_SHAPE;
+  if (T >= kMaxTokens || T * Hq > kMaxRows || B >= kMaxTokens) return PQ1_ERR_SHAPE;
   return PQ1_OK;
 }
 
@@ -268,7 +269,7 @@ pq1_status pq1_paged_attention(const pq1_heads* q, const pq1_heads* out,
   if (misaligned(page_table, 4) || misaligned(cu_q, 4) || misaligned(kv_len, 4))
     return PQ1_ERR_ALIGN;
   const pq1::AttnPlan plan =
-      pq1::plan_attention(B, T, Hq, cache->heads, D, max_q, max_kv);
+      pq1::plan_attention(B, T, Hq, cache->heads, D, max_q, max_kv, window);
   if (!plan.fits) return PQ1_ERR_SHAPE;
   if (plan.workspace_bytes > 0) {
     if (workspace == nullptr) return PQ1_ERR_NULL;
@@ -293,10 +294,12 @@ pq1_status pq1_paged_attention(const pq1_heads* q, const pq1_heads* out,
   pq1::AttnArgs a;
   a.q = q->data, a.q_ts = q->token_stride, a.q_hs = q->head_stride;
   a.out = out->data, a.o_ts = out->token_stride, a.o_hs = out->head_stride;
-  a.k_cache = cache->k, a.v_cache = cache->v, a.pages = cache->pages;
+  a.k_cache = cache->k, a.v_cache = cache->v;
+  a.pages = static_cast<int>(cache->pages);
   a.page_shift = log2_of(cache->page_size);
   a.Hk = cache->heads, a.G = Hq / cache->heads, a.D = D;
-  a.table = page_table, a.max_pages = max_pages;
+  a.by_G = pq1::FastDiv(static_cast<uint32_t>(a.G));
+  a.table = page_table, a.max_pages = static_cast<int>(max_pages);
   a.cu_q = cu_q, a.kv_len = kv_len, a.B = B, a.T = T;
   a.scale_log2 = scale_log2;
   a.causal = causal != 0;

@@ -62,11 +62,12 @@ struct AttnArgs {
   int64_t o_ts = 0, o_hs = 0;
   const void* k_cache = nullptr;
   const void* v_cache = nullptr;
-  int64_t pages = 0;
+  int pages = 0;
   int page_shift = 0;
   int Hk = 0, G = 1, D = 0;  // G: query heads of a cache head
+  FastDiv by_G;
   const int32_t* table = nullptr;
-  int64_t max_pages = 0;
+  int max_pages = 0;  // of a sequence, in its row of the table
   const int32_t* cu_q = nullptr;
   const int32_t* kv_len = nullptr;
   int64_t B = 0, T = 0;
@@ -89,7 +90,7 @@ struct AttnPlan {
   bool fits = false;      // the grid is launchable
 };
 AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_q,
-                        int64_t max_kv);
+                        int64_t max_kv, int window = 0);
 hipError_t launch_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
                             void* workspace, hipStream_t s);
 hipError_t launch_attention(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,

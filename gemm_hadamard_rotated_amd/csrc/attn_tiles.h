@@ -20,21 +20,27 @@ struct Seq {
   int kv;      // keys
 };
 
+// The table and the lengths are read through the scalar cache.
+using Const32 = const __attribute__((address_space(4))) int32_t;
+__device__ __forceinline__ int32_t scalar_load(const int32_t* p, int64_t i) {
+  return reinterpret_cast<Const32*>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int64_t b) {
-  int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+  int64_t q0 = scalar_load(a.cu_q, b), q1 = scalar_load(a.cu_q, b + 1);
+  const int kv = scalar_load(a.kv_len, b);
   q0 = q0 < 0 ? 0 : q0 > a.T ? a.T : q0;
   q1 = q1 < q0 ? q0 : q1 > a.T ? a.T : q1;
-  const int kv = a.kv_len[b];
   return {q0, static_cast<int>(q1 - q0), kv < 0 ? 0 : kv > kMaxKeys ? kMaxKeys : kv};
 }
 
-// Keys [lo, hi) that row i sees.
+// Keys [lo, hi) that row i < n sees.
 __device__ __forceinline__ void visible(const AttnArgs& a, const Seq& s, int i, int* lo, int* hi) {
   *lo = 0;
   *hi = s.kv;
   if (a.causal) {
-    const int64_t end = static_cast<int64_t>(s.kv) - s.n + i + 1;
-    *hi = end < 0 ? 0 : static_cast<int>(end);
+    const int end = s.kv - (s.n - 1 - i);
+    *hi = end < 0 ? 0 : end;
     if (a.window > 0 && *hi > a.window) *lo = *hi - a.window;
   }
 }
@@ -44,17 +50,20 @@ __device__ __forceinline__ void visible(const AttnArgs& a, const Seq& s, int i, 
 // the keys and values a workgroup reads.  A tile of such rows sees keys
 // [start, hi); they are cut into parts of `chunk` keys.
 struct Parts {
-  int start;  // rounded down to a key tile
+  int start;  // rounded down to a multiple of 32
   int lo, hi;  // keys that some row sees
   int lo_max, hi_min;  // keys in [lo_max, hi_min) are seen by every row
   int chunk;
-  int count;
+  __device__ __forceinline__ int count() const {
+    const uint32_t keys = hi > start ? hi - start : 0;
+    return static_cast<int>((keys + chunk - 1) / static_cast<uint32_t>(chunk));
+  }
 };
 
 __device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int r0, int rows,
                                             int chunk, int nsplit) {
   const int last = s.n * a.G - 1;
-  const int i0 = r0 / a.G, i1 = (r0 + rows - 1 < last ? r0 + rows - 1 : last) / a.G;
+  const int i0 = a.by_G.div(r0), i1 = a.by_G.div(r0 + rows - 1 < last ? r0 + rows - 1 : last);
   Parts p;
   int lo0, hi0, lo1, hi1;
   visible(a, s, i0, &lo0, &hi0);
@@ -64,12 +73,19 @@ __device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int
   p.hi = hi1;
   p.lo_max = lo1;
   p.hi_min = hi0;
-  const int64_t keys = p.hi > p.start ? static_cast<int64_t>(p.hi) - p.start : 0;
+  p.chunk = chunk;
   // a cache longer than the caller said stretches the parts
-  const int64_t need = (keys + nsplit - 1) / nsplit;
-  p.chunk = need > chunk ? static_cast<int>((need + 31) & ~int64_t{31}) : chunk;
-  p.count = static_cast<int>((keys + p.chunk - 1) / p.chunk);
+  const int64_t room = static_cast<int64_t>(chunk) * nsplit;
+  if (static_cast<int64_t>(p.hi) - p.start > room) {
+    const uint32_t need = (static_cast<uint32_t>(p.hi - p.start) + nsplit - 1) / nsplit;
+    p.chunk = static_cast<int>((need + 31) & ~31u);
+  }
   return p;
+}
+
+// A tile of keys that not every row sees whole, or with a key on no page.
+__device__ __forceinline__ bool is_edge(const Parts& pt, int j0, int keys, bool gone) {
+  return j0 < pt.lo_max || j0 + keys > pt.hi_min || gone;
 }
 
 template <typename T>
@@ -154,16 +170,67 @@ __device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) 
   }
 }
 
+// Bits 15 and 31 of the result say which of two elements is an infinity or NaN
+// (an exponent of ones carries into its sign's place; the other bits are odds
+// and ends).
+constexpr uint32_t kOdd = 0x80008000u;
 template <typename T>
-__device__ __forceinline__ bool not_finite(uint32_t pair) {  // either of two elements
-  constexpr uint32_t e = __is_same(T, bf16) ? 0x7f80u : 0x7c00u;
-  return (pair & e) == e || (pair & (e << 16)) == (e << 16);
+__device__ __forceinline__ uint32_t odd_bits(uint32_t pair) {
+  return __is_same(T, bf16) ? (pair & 0x7f807f80u) + 0x00800080u
+                            : (pair & 0x7c007c00u) + 0x04000400u;
 }
+// The pair with zero in the place of those.
 template <typename T>
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
-  constexpr uint32_t e = __is_same(T, bf16) ? 0x7f80u : 0x7c00u;
-  return ((pair & e) == e ? 0u : pair & 0xffffu) |
-         ((pair & (e << 16)) == (e << 16) ? 0u : pair & 0xffff0000u);
+  const uint32_t b = odd_bits<T>(pair) & kOdd;
+  return pair & ~(b | (b - (b >> 15)));
+}
+
+// Where the values of a tile's edge are not finite, both kernels take them for
+// zero, because times a probability of zero they would be NaN in the rows that
+// do not see them.  Here the rows that do see them add them to their results:
+// rows [r0, r0 + count) of one (sequence, cache head), keys [k0, k1) in tiles
+// of `keys`.  Every thread of the workgroup calls it, after a barrier that
+// follows the stores.
+template <typename T, typename TO>
+__device__ __forceinline__ void put_back(const AttnArgs& a, const Seq& s, const int32_t* table,
+                                         int h, const Parts& pt, int k0, int k1, int keys,
+                                         int64_t r0, int count, int threads, int split,
+                                         bool partial, float* part_o) {
+  const int lane = threadIdx.x & 63;
+  const int Hq = a.Hk * a.G;
+  for (int j0 = k0; j0 < k1; j0 += keys) {
+    const int j = j0 + lane < k1 ? j0 + lane : k1 - 1;
+    const int p = j >> a.page_shift;
+    int page = p < a.max_pages ? table[p] : -1;
+    if (page >= a.pages) page = -1;
+    if (!is_edge(pt, j0, keys, __any(page < 0 && lane < keys))) continue;
+    for (int key = 0; key < keys && j0 + key < k1; ++key) {
+      const int pg = __shfl(page, key);
+      if (pg < 0) continue;
+      const T* src = static_cast<const T*>(a.v_cache) +
+                     (((static_cast<int64_t>(pg) * a.Hk + h) << a.page_shift) +
+                      ((j0 + key) & ((1 << a.page_shift) - 1))) * a.D;
+      for (int e = threadIdx.x; e < count * a.D; e += threads) {
+        const int64_t r = r0 + e / a.D;
+        const int d = e % a.D;
+        const float x = static_cast<float>(src[d]);
+        if (r >= static_cast<int64_t>(s.n) * a.G || __builtin_isfinite(x)) continue;
+        const int i = a.by_G.div(static_cast<uint32_t>(r));
+        int lo, hi;
+        visible(a, s, i, &lo, &hi);
+        if (j0 + key < lo || j0 + key >= hi) continue;
+        const int64_t row = s.q0 + i;
+        const int hq = h * a.G + static_cast<int>(r) - i * a.G;
+        if (partial) {
+          part_o[((split * a.T + row) * Hq + hq) * a.D + d] += x;
+        } else {
+          TO* y = static_cast<TO*>(a.out) + row * a.o_ts + hq * a.o_hs + d;
+          *y = static_cast<TO>(static_cast<float>(*y) + x);
+        }
+      }
+    }
+  }
 }
 
 }  // namespace pq1

@@ -21,51 +21,67 @@ namespace {
 // the same key order.  So the softmax is lane-local but for two exchanges,
 // and neither P nor V goes through LDS: a lane reads 8 keys x 8 dimensions of
 // V, and picking one dimension of the 8 keys is a byte permute of registers.
+//
+// Bound: reading the cache; a call of one token by its fixed cost.  One token
+// at 131071 keys (4 cache heads, D = 256): 103 us, 5.2 TB/s (a large copy
+// reaches 5.1, a cached one more); 64 tokens at 200 to 8000 keys: 232 us, 4.9
+// TB/s; one token at 701 keys: 8 us for this kernel and 4.6 for the join, where
+// an empty kernel takes 3.  What paid: as many workgroups as CUs (twice as
+// many: 109 and 239 us), divisions by multiplication, lengths and page numbers
+// through the scalar cache, runs of 16 keys as buffers whose end cuts off the
+// keys past the last (31 KB of code became 13; one token 11.3 -> 8.0 us, drafts
+// of 16 users in a window of 1024 keys 34 -> 22 us).  Two workgroups a CU where
+// registers allow (D < 256; at 256 they spill: 240 -> 375 us).
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 32;   // keys of a tile
 constexpr int kWaves = 4;
 
 struct FewGrid {
   int row_tiles, nsplit, chunk;
+  FastDiv by_tiles, by_split, by_Hk;
 };
 
-// Rows of the cache that hold a tile's keys.  With pages of at least a tile
-// (UNI) they are one run; else every lane keeps the page of one key.
+// Where a tile's 32 keys are.  With pages of 16 keys or more (RUNS) they are
+// two runs of 16 rows; else every lane keeps the page of one key.
 struct TileAt {
-  int64_t row;  // UNI: cache row of the first key
-  int page;     // not UNI: page of key lane % 32
-  bool bad;     // a key some row sees lies on no page of the cache
+  int64_t row[2];  // RUNS: cache rows of keys 0 and 16
+  int keys[2];     // RUNS: keys there, none on a page that is not the cache's
+  int page;        // not RUNS: page of key lane % 32, -1 for none
+  uint32_t gone;   // visible keys on no page of the cache
 };
 
-template <bool UNI>
+template <bool RUNS>
 __device__ __forceinline__ TileAt find_tile(const AttnArgs& a, const int32_t* table, int h, int j0,
                                             int hi, int lane) {
-  TileAt t;
+  TileAt t{};
   const int mask = (1 << a.page_shift) - 1;
-  if (UNI) {
-    const int p = j0 >> a.page_shift;
-    const int page = p < a.max_pages ? table[p] : -1;
-    t.bad = page < 0 || page >= a.pages;
-    t.row = ((static_cast<int64_t>(t.bad ? 0 : page) * a.Hk + h) << a.page_shift) + (j0 & mask);
-    t.page = 0;
+  if constexpr (RUNS) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = j0 + 16 * e, p = j >> a.page_shift;
+      int page = -1, keys = hi - j < 16 ? hi - j : 16;
+      if (keys > 0 && p < a.max_pages) page = scalar_load(table, p);
+      if (page < 0 || page >= a.pages) {
+        if (keys > 0) t.gone |= (1u << keys) - 1 << 16 * e;
+        page = keys = 0;
+      }
+      t.row[e] = ((static_cast<int64_t>(page) * a.Hk + h) << a.page_shift) + (j & mask);
+      t.keys[e] = keys;
+    }
   } else {
     const int j = j0 + (lane & 31);
     const int p = j >> a.page_shift;
-    int page = 0;
-    bool bad = false;
     if (j < hi) {
-      page = p < a.max_pages ? table[p] : -1;
-      bad = page < 0 || page >= a.pages;
+      t.page = p < a.max_pages ? table[p] : -1;
+      if (t.page >= a.pages) t.page = -1;
     }
-    t.page = bad ? -1 : page;
-    t.bad = __any(bad);
-    t.row = 0;
+    t.gone = static_cast<uint32_t>(__ballot(t.page < 0));
   }
   return t;
 }
 
-template <typename T, typename TO, int D, int RB, bool UNI>
-__global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(AttnArgs a, FewGrid fg,
+template <typename T, typename TO, int D, int RB, bool RUNS>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void few_rows_kernel(AttnArgs a, FewGrid fg,
                                                                float* part_o, float2* part_ml) {
   constexpr int NP = kParts<T, TO>;
   constexpr int DV = D >= 128 ? 8 : 4;     // dimensions of V a lane reads at once
@@ -75,37 +91,36 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(AttnArgs a, FewGr
   using VReg = __attribute__((ext_vector_type(DV / 2))) uint32_t;
   __shared__ __attribute__((aligned(16))) float sum_o[kWaves][16][D + 4];
   __shared__ float sum_m[kWaves][16], sum_l[kWaves][16];
+  __shared__ int odd_of[kWaves];
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  uint32_t id = blockIdx.x;
-  const int split = id % fg.nsplit;
-  id /= fg.nsplit;
-  const int rt = id % fg.row_tiles;
-  id /= fg.row_tiles;
-  const int h = id % a.Hk;
-  const int b = id / a.Hk;
+  const uint32_t id0 = fg.by_split.div(blockIdx.x), split = blockIdx.x - id0 * fg.by_split.d;
+  const uint32_t id1 = fg.by_tiles.div(id0), rt = id0 - id1 * fg.by_tiles.d;
+  const uint32_t b = fg.by_Hk.div(id1);
+  const int h = id1 - b * fg.by_Hk.d;
   const Seq s = load_seq(a, b);
-  const int32_t* table = a.table + b * a.max_pages;
+  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
   const int rows = s.n * a.G;
   const int Hq = a.Hk * a.G;
 
   for (int64_t r0 = static_cast<int64_t>(rt) * ROWS; r0 < rows;
        r0 += static_cast<int64_t>(fg.row_tiles) * ROWS) {
     const Parts pt = split_keys(a, s, static_cast<int>(r0), ROWS, fg.chunk, fg.nsplit);
-    if (split > 0 && split >= pt.count) continue;
-    const int k0 = pt.start + split * pt.chunk;
+    const int64_t from = pt.start + static_cast<int64_t>(split) * pt.chunk;
+    if (split > 0 && from >= pt.hi) continue;
+    const int k0 = static_cast<int>(from);
     const int k1 = pt.hi - k0 < pt.chunk ? pt.hi : k0 + pt.chunk;
-    const bool one_token = r0 / a.G == ((r0 + ROWS < rows ? r0 + ROWS : rows) - 1) / a.G;
+    // rows of one token see the same keys
+    const bool one_token = pt.lo == pt.lo_max && pt.hi == pt.hi_min;
+    bool odd_values = false;  // infinities or NaN were taken out of V
 
-    int lo[RB], hi[RB];
     U4 q[RB][D / 32];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
       const int r = static_cast<int>(r0) + 16 * rb + col;
-      lo[rb] = hi[rb] = 0;
-      const int i = r / a.G;
-      if (r < rows) visible(a, s, i, &lo[rb], &hi[rb]);
+      const int i = a.by_G.div(r);
       const T* src = static_cast<const T*>(a.q) + (s.q0 + i) * a.q_ts +
                      (h * a.G + r - i * a.G) * a.q_hs + 8 * g;
 #pragma unroll
@@ -124,63 +139,51 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(AttnArgs a, FewGr
 
     U4 kr[2][D / 32];
     VReg vr[8][CH];
-    // Past the last tile nothing is fetched: a buffer of no records, or the
-    // wave's last tile again.
+    auto run_of = [&](const void* cache, const TileAt& t, int e) {
+      return __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<T*>(static_cast<const T*>(cache) + t.row[e] * D), 0, t.keys[e] * D * 2,
+          0x00020000);
+    };
+    auto row_of = [&](const TileAt& t, int j0, int key) {
+      const int page = __shfl(t.page, key);
+      return ((static_cast<int64_t>(page < 0 ? 0 : page) * a.Hk + h) << a.page_shift) +
+             ((j0 + key) & ((1 << a.page_shift) - 1));
+    };
+    // Keys past the last read as zeros (RUNS) or as some row of the cache.
     auto load_k = [&](const TileAt& t, int j0) {
-      if constexpr (UNI) {
-        const int left = j0 < k1 ? pt.hi - j0 : 0;
-        const auto buf = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<T*>(static_cast<const T*>(a.k_cache) + t.row * D), 0,
-            (left < kKeys ? left : kKeys) * D * 2, 0x00027000);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (RUNS) {
+          const auto run = run_of(a.k_cache, t, e);
 #pragma unroll
           for (int d = 0; d < D / 32; ++d)
-            kr[e][d] = __builtin_amdgcn_raw_buffer_load_b128(
-                buf, ((16 * e + col) * D + 8 * g + 32 * d) * 2, 0, 0);
-      } else {
+            kr[e][d] =
+                __builtin_amdgcn_raw_buffer_load_b128(run, (col * D + 8 * g + 32 * d) * 2, 0, 0);
+        } else {
+          const T* src = static_cast<const T*>(a.k_cache) + row_of(t, j0, 16 * e + col) * D + 8 * g;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = 16 * e + col;
-          const int page = __shfl(t.page, key);
-          const int64_t row =
-              ((static_cast<int64_t>(page < 0 ? 0 : page) * a.Hk + h) << a.page_shift) +
-              ((j0 + key) & ((1 << a.page_shift) - 1));
-          const T* src = static_cast<const T*>(a.k_cache) + row * D + 8 * g;
-#pragma unroll
-          for (int d = 0; d < D / 32; ++d)
-            kr[e][d] = *reinterpret_cast<const U4*>(src + 32 * d);
+          for (int d = 0; d < D / 32; ++d) kr[e][d] = *reinterpret_cast<const U4*>(src + 32 * d);
         }
       }
     };
     auto load_v = [&](const TileAt& t, int j0) {
-      if constexpr (UNI) {
-        const int left = pt.hi - j0;
-        const auto buf = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<T*>(static_cast<const T*>(a.v_cache) + t.row * D), 0,
-            (left < kKeys ? left : kKeys) * D * 2, 0x00027000);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (RUNS) {
+          const auto run = run_of(a.v_cache, t, e >> 2);
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
-            const int at = ((12 * (e >> 2) + e + 4 * g) * D + DV * col + 16 * DV * c) * 2;
+            const int at = (((e & 3) + 4 * g) * D + DV * col + 16 * DV * c) * 2;
             if constexpr (DV == 8)
-              vr[e][c] = __builtin_amdgcn_raw_buffer_load_b128(buf, at, 0, 0);
+              vr[e][c] = __builtin_amdgcn_raw_buffer_load_b128(run, at, 0, 0);
             else
-              vr[e][c] = __builtin_amdgcn_raw_buffer_load_b64(buf, at, 0, 0);
+              vr[e][c] = __builtin_amdgcn_raw_buffer_load_b64(run, at, 0, 0);
           }
-      } else {
+        } else {
+          const T* src = static_cast<const T*>(a.v_cache) +
+                         row_of(t, j0, 12 * (e >> 2) + e + 4 * g) * D + DV * col;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int key = 12 * (e >> 2) + e + 4 * g;
-          const int page = __shfl(t.page, key);
-          const int64_t row =
-              ((static_cast<int64_t>(page < 0 ? 0 : page) * a.Hk + h) << a.page_shift) +
-              ((j0 + key) & ((1 << a.page_shift) - 1));
-          const T* src = static_cast<const T*>(a.v_cache) + row * D + DV * col;
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-            vr[e][c] = *reinterpret_cast<const VReg*>(src + 16 * DV * c);
+          for (int c = 0; c < CH; ++c) vr[e][c] = *reinterpret_cast<const VReg*>(src + 16 * DV * c);
         }
       }
     };
@@ -188,66 +191,75 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(AttnArgs a, FewGr
     int j0 = k0 + kKeys * wave;
     TileAt at{};
     if (j0 < k1) {
-      at = find_tile<UNI>(a, table, h, j0, pt.hi, lane);
+      at = find_tile<RUNS>(a, table, h, j0, pt.hi, lane);
       load_k(at, j0);
     }
+#pragma unroll 1
     for (; j0 < k1; j0 += kKeys * kWaves) {
       load_v(at, j0);
+      // past the last tile nothing is fetched, or the same tile again
       const int jn = j0 + kKeys * kWaves;
-      TileAt next = at;
-      if (jn < k1) next = find_tile<UNI>(a, table, h, jn, pt.hi, lane);
+      const TileAt next = find_tile<RUNS>(a, table, h, RUNS || jn < k1 ? jn : j0,
+                                          RUNS ? k1 : pt.hi, lane);
 
       F4 sc[RB][2];
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          sc[rb][e] = F4{0, 0, 0, 0};
-#pragma unroll
-          for (int d = 0; d < D / 32; ++d)
-            sc[rb][e] = mfma16(kr[e][d], q[rb][d], sc[rb][e], T{});
-        }
-      load_k(next, jn < k1 ? jn : UNI ? k1 : j0);
-
-      // A tile that not every row sees whole, or with a page missing
-      const bool edge = j0 < pt.lo_max || j0 + kKeys > pt.hi_min || at.bad;
-      bool patch = false;  // rows add this tile's infinities and NaN one by one
-      if (edge) {
-        bool odd = false;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int key = 12 * (e >> 2) + e + 4 * g;
-          const bool gone = UNI ? at.bad : __shfl(at.page, key) < 0;
-          const bool seen = j0 + key >= pt.lo && j0 + key < pt.hi && !gone;
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int w = 0; w < DV / 2; ++w) {
-              vr[e][c][w] = seen ? vr[e][c][w] : 0u;
-              odd |= not_finite<T>(vr[e][c][w]);
-            }
-        }
-        patch = __any(odd) && !one_token;
-        if (patch) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-              for (int w = 0; w < DV / 2; ++w) vr[e][c][w] = finite_or_zero<T>(vr[e][c][w]);
-        }
+      for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = 16 * e + 4 * g + i;
-            const bool gone = UNI ? at.bad : __shfl(at.page, key) < 0;
+          for (int rb = 0; rb < RB; ++rb)
+            sc[rb][e] = mfma16(kr[e][d], q[rb][d], d == 0 ? F4{0, 0, 0, 0} : sc[rb][e], T{});
+      load_k(next, RUNS || jn < k1 ? jn : j0);
+
+      if (is_edge(pt, j0, kKeys, at.gone != 0)) {
+        // Values no row sees become zero, and where rows see different keys
+        // infinities and NaN among the others too (put_back).
+        if (!RUNS || !one_token || j0 < pt.lo) {
+          const int lo = pt.lo - j0 - 4 * g, hi = pt.hi - j0 - 4 * g;
+          const uint32_t gone = at.gone >> 4 * g;
+          uint32_t odd = 0;
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-              const bool seen = j0 + key >= lo[rb] && j0 + key < hi[rb];
-              sc[rb][e][i] = !seen ? kNegInf : gone ? __builtin_nanf("") : sc[rb][e][i];
-            }
+          for (int e = 0; e < 8; ++e) {
+            const int key = 12 * (e >> 2) + e;
+            const uint32_t seen =
+                key >= lo && key < hi && (gone >> key & 1) == 0 ? 0xffffffffu : 0u;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+              for (int w = 0; w < DV / 2; ++w) {
+                vr[e][c][w] &= seen;
+                odd |= odd_bits<T>(vr[e][c][w]);
+              }
           }
+          if (!one_token && __any((odd & kOdd) != 0)) {
+            odd_values = true;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+              for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int w = 0; w < DV / 2; ++w) vr[e][c][w] = finite_or_zero<T>(vr[e][c][w]);
+          }
+        }
+        const uint32_t gone = at.gone >> 4 * g;
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          const int r = static_cast<int>(r0) + 16 * rb + col;
+          int lo = 0, hi = 0;
+          if (r < rows) visible(a, s, a.by_G.div(r), &lo, &hi);
+          lo -= j0 + 4 * g;
+          hi -= j0 + 4 * g;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = 16 * e + i;
+              sc[rb][e][i] = key < lo || key >= hi    ? kNegInf
+                             : (gone >> key & 1) != 0 ? __builtin_nanf("")
+                                                      : sc[rb][e][i];
+            }
+        }
       }
 
       U4 pr[RB][NP];
@@ -296,30 +308,6 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(AttnArgs a, FewGr
                 o[rb][c * DV + 2 * w + z] =
                     mfma16(f, pr[rb][n], o[rb][c * DV + 2 * w + z], T{});
           }
-      if (patch) {
-        for (int key = 0; key < kKeys; ++key) {
-          const int page = UNI ? 0 : __shfl(at.page, key);
-          const int64_t row =
-              UNI ? at.row + key
-                  : ((static_cast<int64_t>(page) * a.Hk + h) << a.page_shift) +
-                        ((j0 + key) & ((1 << a.page_shift) - 1));
-          if (j0 + key >= pt.hi || page < 0 || (UNI && at.bad)) continue;
-          const T* src = static_cast<const T*>(a.v_cache) + row * D;
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb)
-            if (j0 + key >= lo[rb] && j0 + key < hi[rb]) {
-#pragma unroll
-              for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int z = 0; z < DV; ++z)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const float x = static_cast<float>(src[16 * DV * c + DV * (4 * g + i) + z]);
-                    if (!__builtin_isfinite(x)) o[rb][c * DV + z][i] += x;
-                  }
-            }
-        }
-      }
       at = next;
     }
 
@@ -327,18 +315,18 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(AttnArgs a, FewGr
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
       const float ls = sum_groups(l[rb]);
-      __syncthreads();
+      if (rb > 0) __syncthreads();
       if (g == 0) {
         sum_m[wave][col] = m[rb];
         sum_l[wave][col] = ls;
       }
+      if (lane == 0) odd_of[wave] = odd_values;
       __syncthreads();
       float top = kNegInf;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sum_m[w][col]);
-      const float keep = m[rb] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[rb] - top);
       // a wave without a finite score still hands on its NaN
-      const float f = m[rb] == kNegInf ? 1.0f : keep;
+      const float f = m[rb] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[rb] - top);
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -364,7 +352,7 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(AttnArgs a, FewGr
           lx += sum_l[w][row] * (mw == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(mw - mx));
           x += *reinterpret_cast<const F4*>(&sum_o[w][row][d]);
         }
-        const int i = r / a.G;
+        const int i = a.by_G.div(r);
         const int hq = h * a.G + r - i * a.G;
         if (fg.nsplit > 1) {
           const int64_t at_row = static_cast<int64_t>(split) * a.T * Hq + (s.q0 + i) * Hq + hq;
@@ -381,6 +369,11 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(AttnArgs a, FewGr
       }
     }
     __syncthreads();
+    if (!one_token && (odd_of[0] | odd_of[1] | odd_of[2] | odd_of[3])) {
+      put_back<T, TO>(a, s, table, h, pt, k0, k1, kKeys, r0, ROWS, 64 * kWaves, split,
+                      fg.nsplit > 1, part_o);
+      __syncthreads();
+    }
   }
 }
 
@@ -393,27 +386,29 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, FewGrid fg, int t
   constexpr int N = D / 64;
   const int lane = threadIdx.x & 63;
   const int Hq = a.Hk * a.G;
-  const int heads4 = (Hq + 3) / 4;
-  uint32_t id = blockIdx.x;
-  const int hq = (id % heads4) * 4 + (threadIdx.x >> 6);
-  id /= heads4;
-  const int b = id / tokens;
+  const uint32_t heads4 = (Hq + 3) / 4;
+  const uint32_t id = blockIdx.x / heads4;
+  const int hq = (blockIdx.x - id * heads4) * 4 + (threadIdx.x >> 6);
+  const uint32_t b = id / static_cast<uint32_t>(tokens);
   const Seq s = load_seq(a, b);
   if (hq >= Hq) return;
   const int64_t stride = a.T * Hq;
-  for (int i = id % tokens; i < s.n; i += tokens) {
-    const int r = i * a.G + hq % a.G;
-    const Parts pt = split_keys(a, s, r / tile_rows * tile_rows, tile_rows, fg.chunk, fg.nsplit);
+  const int hq_in = hq - static_cast<int>(a.by_G.div(hq)) * a.G;
+  for (int i = id - b * tokens; i < s.n; i += tokens) {
+    const int r = i * a.G + hq_in;
+    // a tile's rows are a power of two
+    const Parts pt = split_keys(a, s, r & -tile_rows, tile_rows, fg.chunk, fg.nsplit);
+    const int count = pt.count();
     int lo, hi;
     visible(a, s, i, &lo, &hi);
     const int64_t row = (s.q0 + i) * Hq + hq;
     float top = kNegInf;
-    for (int p = lane; p < pt.count; p += 64) top = fmaxf(top, part_ml[p * stride + row].x);
+    for (int p = lane; p < count; p += 64) top = fmaxf(top, part_ml[p * stride + row].x);
 #pragma unroll
     for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
     float acc[N] = {}, l = 0.0f;
 #pragma unroll 8
-    for (int p = 0; p < pt.count; ++p) {
+    for (int p = 0; p < count; ++p) {
       const float2 ml = part_ml[p * stride + row];
       const float w = ml.x == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
       float x[N];
@@ -428,15 +423,21 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, FewGrid fg, int t
   }
 }
 
+FewGrid grid_of(const AttnPlan& plan, const AttnArgs& a) {
+  return {static_cast<int>(plan.row_tiles), plan.nsplit, plan.chunk,
+          FastDiv(static_cast<uint32_t>(plan.row_tiles)),
+          FastDiv(static_cast<uint32_t>(plan.nsplit)), FastDiv(static_cast<uint32_t>(a.Hk))};
+}
+
 template <typename T, typename TO, int D, int RB>
 hipError_t launch_few(const AttnPlan& plan, const AttnArgs& a, void* workspace, hipStream_t s) {
-  const FewGrid fg{static_cast<int>(plan.row_tiles), plan.nsplit, plan.chunk};
+  const FewGrid fg = grid_of(plan, a);
   float* part_o = static_cast<float*>(workspace);
   float2* part_ml =
       reinterpret_cast<float2*>(part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
   const dim3 grid(static_cast<uint32_t>(a.B * a.Hk * plan.row_tiles * plan.nsplit));
-  // pages of a whole key tile or more are read as one run
-  if (a.page_shift >= 5)
+  // pages of half a key tile or more are read as runs
+  if (a.page_shift >= 4)
     few_rows_kernel<T, TO, D, RB, true><<<grid, 64 * kWaves, 0, s>>>(a, fg, part_o, part_ml);
   else
     few_rows_kernel<T, TO, D, RB, false><<<grid, 64 * kWaves, 0, s>>>(a, fg, part_o, part_ml);
@@ -445,7 +446,7 @@ hipError_t launch_few(const AttnPlan& plan, const AttnArgs& a, void* workspace, 
 
 template <typename TO, int D>
 hipError_t launch_join(const AttnPlan& plan, const AttnArgs& a, void* workspace, hipStream_t s) {
-  const FewGrid fg{static_cast<int>(plan.row_tiles), plan.nsplit, plan.chunk};
+  const FewGrid fg = grid_of(plan, a);
   const float* part_o = static_cast<const float*>(workspace);
   const float2* part_ml = reinterpret_cast<const float2*>(
       part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
@@ -481,14 +482,31 @@ hipError_t join_parts(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStre
   }
 }
 
-// A sequence's longest chunk has up to this many rows of a cache head in the
-// few-rows kernel, more in the many-rows one.
-constexpr int64_t kFewRows = 64;
+// Which kernel: estimated times, in ns, of a call whose work fills the device.
+// A CU takes 0.19 D ns a key for a 32-row tile of the few-rows kernel, whose
+// start costs as much as 130 keys, and 20 + 0.16 D ns a key for a 256-row tile
+// of the other, which needs 7 us more before its first key.  At D = 128, 8
+// cache heads, few rows against many: 64 sequences of 1000 keys, 24 rows 46 and
+// 82 us, 72 rows 120 and 87; one sequence of 8000 keys, 48 rows 18 and 28, 144
+// rows 44 and 31; of 500 keys, 384 rows 14 and 25.
+bool prefer_many(int64_t units, int64_t rows, int64_t keys, int D) {
+  const double per_cu = static_cast<double>(units) / 256;
+  const double few = static_cast<double>((rows + 31) / 32) * per_cu * (keys + 130.0) * 0.19 * D;
+  const double many = static_cast<double>((rows + kTileRows - 1) / kTileRows) * per_cu * keys *
+                          (20 + 0.16 * D) + 7000;
+  return rows > 32 && many < few;
+}
+
+// Up to this many elements of K a head's keys stay in one part where rows are
+// few: one launch.  One token of 4 cache heads at D = 256, calls one after
+// another: 300 keys 10.9 us in one part and 14.7 in several, 700 keys 17.4 and
+// 14.6; at D = 128 700 keys 10.8 and 14.5, 1500 keys 16.7 and 14.7.
+constexpr int64_t kShort = 98304;
 
 }  // namespace
 
 AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_q,
-                        int64_t max_kv) {
+                        int64_t max_kv, int window) {
   // A launch holds less than 2^32 threads.  Kernels walk on over rows that
   // their grid has no workgroup for, so a long chunk only costs balance.
   constexpr int64_t most = (int64_t{1} << 32) / (2 * kTileRows) - 1;
@@ -498,29 +516,39 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max
   p.fits = true;
   p.tokens = max_q < 1 ? 1 : max_q < T ? max_q : T;
   const int64_t rows = p.tokens * (Hq / Hk);
-  p.many = rows > kFewRows;
+  int64_t kv = max_kv < 1 ? 1 : max_kv > 0x7fffffff ? 0x7fffffff : max_kv;
+  p.many = prefer_many(B * Hk, rows, kv, D);
   p.tile_rows = p.many ? kTileRows : rows <= 16 ? 16 : 32;
   p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   if (p.row_tiles > most / (B * Hk)) p.row_tiles = most / (B * Hk);
-  const int64_t kv = max_kv < 1 ? 1 : max_kv > 0x7fffffff ? 0x7fffffff : max_kv;
   const int64_t units = B * Hk * p.row_tiles;
   const int64_t step = kKeys * kWaves;
-  int64_t parts = 1;
-  if (p.many) {
-    // One workgroup to a CU: as many parts as the device takes at once.  More,
-    // to even out a last round, cost more than they give (192 workgroups of
-    // 7168 keys: 396 us; in 4 parts, three full rounds: 407 us and 48 to join
-    // them): idle CUs leave the others a higher clock.
-    while (units * (parts + 1) <= cus && (parts + 1) * 256 <= kv) ++parts;
-  } else if (units < 2 * cus) {
-    // Enough workgroups for two on each CU, but no part shorter than one key
-    // tile for each wave.
-    parts = (2 * cus + units - 1) / units;
-  }
-  int64_t chunk = ((kv + parts - 1) / parts + step - 1) / step * step;
+  auto cut = [&](int64_t keys) {  // parts of that many keys
+    int64_t parts = 1;
+    if (p.many) {
+      // One workgroup to a CU: as many parts as the device takes at once.
+      // More, to even out a last round, cost more than they give (192
+      // workgroups of 7168 keys: 396 us; in 4 parts, three full rounds: 407 us
+      // and 48 to join them): idle CUs leave the others a higher clock.
+      while (units * (parts + 1) <= cus && (parts + 1) * 256 <= keys) ++parts;
+    } else if (units < cus && keys * D > kShort) {
+      parts = (cus + units - 1) / units;
+    }
+    // no part shorter than one key tile for each wave
+    const int64_t most_parts = (keys + step - 1) / step;
+    return parts < most_parts ? parts : most_parts;
+  };
+  // The workspace is for all keys, of which a window may leave fewer (a tile's
+  // rows see the window's keys, one more for each row after the first, and the
+  // start is rounded down): no more parts, shorter ones.
+  const int64_t parts = cut(kv);
+  p.workspace_bytes = parts > 1 ? static_cast<size_t>(parts) * T * Hq * (D * 4 + 8) : 0;
+  const int64_t reach = int64_t{window} + p.tile_rows + 64;
+  if (window > 0 && reach < kv) kv = reach;
+  const int64_t n = cut(kv);
+  const int64_t chunk = ((kv + n - 1) / n + step - 1) / step * step;
   p.chunk = chunk > 0x7fffff00 ? 0x7fffff00 : static_cast<int>(chunk);
   p.nsplit = static_cast<int>((kv + p.chunk - 1) / p.chunk);
-  p.workspace_bytes = p.nsplit > 1 ? static_cast<size_t>(p.nsplit) * T * Hq * (D * 4 + 8) : 0;
   return p;
 }
 

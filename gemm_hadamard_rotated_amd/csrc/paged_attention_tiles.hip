@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
   const int b = id % a.B;
   const int rt = tg.row_tiles - 1 - static_cast<int>(id / a.B);
   const Seq s = load_seq(a, b);
-  const int32_t* table = a.table + b * a.max_pages;
+  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
   const int rows = s.n * a.G;
   const int Hq = a.Hk * a.G;
   const int page_mask = (1 << a.page_shift) - 1;
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
   for (int64_t r0 = static_cast<int64_t>(rt) * kTileRows; r0 < rows;
        r0 += static_cast<int64_t>(tg.row_tiles) * kTileRows) {
     const Parts pt = split_keys(a, s, static_cast<int>(r0), kTileRows, tg.chunk, tg.nsplit);
-    if (split > 0 && split >= pt.count) continue;
+    if (split > 0 && split >= pt.count()) continue;
     const int k0 = pt.start + split * pt.chunk;
     const int k1 = pt.hi - k0 < pt.chunk ? pt.hi : k0 + pt.chunk;
 
@@ -139,13 +139,13 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
     if (wr0 < rows) {
       int t;
       const int last = (wr0 + 32 < rows ? wr0 + 32 : rows) - 1;
-      visible(a, s, wr0 / a.G, &wlo, &t);
-      visible(a, s, last / a.G, &t, &whi);
+      visible(a, s, a.by_G.div(wr0), &wlo, &t);
+      visible(a, s, a.by_G.div(last), &t, &whi);
     }
     U4 q[D / 16];
     {
       const int r = wr0 + col;
-      const int i = r / a.G;
+      const int i = a.by_G.div(r);
       const T* src = static_cast<const T*>(a.q) + (s.q0 + i) * a.q_ts +
                      (h * a.G + r - i * a.G) * a.q_hs + 8 * g;
 #pragma unroll
@@ -190,15 +190,11 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
                vb + to);
       }
     };
-    // A tile that not every row sees whole, or with a page missing
-    auto is_edge = [&](int j0, uint64_t gone) {
-      return j0 < pt.lo_max || j0 + KT > pt.hi_min || gone != 0;
-    };
     // Values no row sees become zero, and where there are infinities or NaN
     // among the others these too: times a probability of zero they would be
     // NaN in the rows that do not see them.
     auto clean = [&](char* vb, int j0, uint64_t gone) {
-      bool odd = false;
+      uint32_t odd = 0;
 #pragma unroll
       for (int e = 0; e < TILE / 16 / (64 * kTileWaves); ++e) {
         const int at = 64 * kTileWaves * e + here(threadIdx.x);
@@ -209,12 +205,12 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           x[w] = seen ? x[w] : 0u;
-          odd |= not_finite<T>(x[w]);
+          odd |= odd_bits<T>(x[w]);
           x[w] = finite_or_zero<T>(x[w]);
         }
         *v = x;
       }
-      odd_values |= __syncthreads_or(odd) != 0;
+      odd_values |= __syncthreads_or((odd & kOdd) != 0) != 0;
     };
 
     const int kat = col * ROWB + 16 * (g ^ k_bits<D>(col));
@@ -254,13 +250,13 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
 
     // Softmax of the scores, O^T += V^T P^T.
     auto products = [&](const char* vb, int j0, uint64_t gone, F16 (&sc)[EB]) {
-      if (is_edge(j0, gone)) {
+      if (is_edge(pt, j0, KT, gone != 0)) {
         // key numbers relative to the lane's first: compile-time constants
         const int at = j0 + 4 * g;
         const uint64_t lost = gone >> (4 * g);
         int lo = 0, hi = 0;
         const int r = wr0 + here(lane) % 32;
-        if (r < rows) visible(a, s, r / a.G, &lo, &hi);
+        if (r < rows) visible(a, s, a.by_G.div(r), &lo, &hi);
         lo -= at;
         hi -= at;
 #pragma unroll
@@ -360,7 +356,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
 #pragma unroll 1
       for (int j0 = first; j0 < end; j0 += KT) {
         const uint64_t gone = any_gone ? gone_of(j0) : 0;
-        if (is_edge(j0, gone)) clean(v_lds + now, j0, gone);
+        if (is_edge(pt, j0, KT, gone != 0)) clean(v_lds + now, j0, gone);
         copy(page, j0 + 2 * KT, k_lds + then, v_lds + then);
         find_pages(j0 + 3 * KT, page);
         F16 sc[EB];
@@ -380,7 +376,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
       const float sum = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
       const int r = wr0 + col;
       if (r < rows) {
-        const int i = r / a.G;
+        const int i = a.by_G.div(r);
         const int hq = h * a.G + r - i * a.G;
         const int64_t at_row = static_cast<int64_t>(split) * a.T * Hq + (s.q0 + i) * Hq + hq;
         if (tg.nsplit > 1 && g == 0) part_ml[at_row] = make_float2(m, sum);
@@ -406,39 +402,10 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
       }
     }
 
-    // Put back what the tiles' edges took out: rows that see an infinity or
-    // NaN add it to their result.
     if (odd_values) {
       __syncthreads();
-      for (int j0 = k0; j0 < k1; j0 += KT) {
-        const int j = j0 + lane < k1 ? j0 + lane : k1 - 1;
-        const int p = j >> a.page_shift;
-        int page = p < a.max_pages ? table[p] : -1;
-        if (page >= a.pages) page = -1;
-        if (!is_edge(j0, __any(page < 0))) continue;
-        for (int key = 0; key < KT && j0 + key < k1; ++key) {
-          const int pg = __shfl(page, key);
-          if (pg < 0) continue;
-          const T* src = static_cast<const T*>(a.v_cache) + row_of(pg, j0 + key) * D;
-          for (int e = threadIdx.x; e < kTileRows * D; e += 64 * kTileWaves) {
-            const int64_t r = r0 + e / D;
-            const int d = e % D;
-            const float x = static_cast<float>(src[d]);
-            if (r >= rows || __builtin_isfinite(x)) continue;
-            const int i = static_cast<int>(r) / a.G;
-            int rlo, rhi;
-            visible(a, s, i, &rlo, &rhi);
-            if (j0 + key < rlo || j0 + key >= rhi) continue;
-            const int hq = h * a.G + static_cast<int>(r) - i * a.G;
-            if (tg.nsplit > 1) {
-              part_o[(static_cast<int64_t>(split) * a.T * Hq + (s.q0 + i) * Hq + hq) * D + d] += x;
-            } else {
-              TO* y = static_cast<TO*>(a.out) + (s.q0 + i) * a.o_ts + hq * a.o_hs + d;
-              *y = static_cast<TO>(static_cast<float>(*y) + x);
-            }
-          }
-        }
-      }
+      put_back<T, TO>(a, s, table, h, pt, k0, k1, KT, r0, kTileRows, 64 * kTileWaves, split,
+                      tg.nsplit > 1, part_o);
     }
     __syncthreads();  // the next tile of rows takes the buffers
   }

@@ -467,8 +467,8 @@ pq1_status pq1_kv_append(const pq1_heads* k, const pq1_heads* v, const int64_t* 
  *              aligned; may be NULL where that is 0.  Its content does not
  *              matter and is not kept; calls that may overlap in time need
  *              different workspaces.
- *   dim is 64, 128 or 256; Hq a multiple of the cache's heads; T * Hq and the
- *   pages' row count (pages * heads * page_size) below 2^31 and 2^40.
+ *   dim is 64, 128 or 256; Hq a multiple of the cache's heads; T * Hq is
+ *   at most 0x7ff00000, the pages' row count (pages * heads * page_size) 2^40.
  * Results do not depend on scheduling: the key range is split by the call's
  * sizes alone and the parts are joined in order.  Probabilities enter the
  * second product as the cache's type (for an fp32 result as two or three such

@@ -173,6 +173,11 @@ def test_append(pq, dev, case):
 # ---------------------------------------------------------------------------
 # Attention
 # ---------------------------------------------------------------------------
+# The longest kv_len that a call states decides, with the number of rows, which
+# kernel takes it; any statement has to give right results.
+STATED = [1, 10 ** 6]
+
+
 class Batch:
     """B sequences over a shuffled paged cache; everything unread is NaN."""
 
@@ -261,11 +266,12 @@ ATTN = [
 def test_attention(pq, dev, case):
     qs, kvs, Hk, G, D, page, dt, dout, causal, window = case
     s = Batch(pq, dev, qs, kvs, Hk, G, D, page, dt)
-    got = s.run(causal=causal, window=window, out_dtype=dout)
-    assert got.dtype == dout
-    s.check(got, causal, window)
-    again = s.run(causal=causal, window=window, out_dtype=dout)
-    assert torch.equal(got, again), "the same call gives the same bits"
+    for stated in [None] + STATED:
+        got = s.run(max_kv=stated, causal=causal, window=window, out_dtype=dout)
+        assert got.dtype == dout
+        s.check(got, causal, window, where=f"stated {stated}")
+        again = s.run(max_kv=stated, causal=causal, window=window, out_dtype=dout)
+        assert torch.equal(got, again), "the same call gives the same bits"
 
 
 def test_attention_scale_and_far_scores(pq, dev):
@@ -274,10 +280,13 @@ def test_attention_scale_and_far_scores(pq, dev):
         s = Batch(pq, dev, [rows], [640], 1, 2, 64, 16, F16, seed=rows, peaked=6.0)
         s.k[0] *= torch.linspace(0.05, 4.0, 640).view(-1, 1, 1).to(F16)
         s.fill()
-        s.check(s.run(scale=0.7, out_dtype=F32), scale=0.7, where=f"{rows} rows, rising")
+        for kv in STATED:
+            s.check(s.run(max_kv=kv, scale=0.7, out_dtype=F32), scale=0.7,
+                    where=f"{rows} rows, rising")
         s.k[0] = s.k[0].flip(0).contiguous()
         s.fill()
-        s.check(s.run(scale=0.7), scale=0.7, where=f"{rows} rows, falling")
+        for kv in STATED:
+            s.check(s.run(max_kv=kv, scale=0.7), scale=0.7, where=f"{rows} rows, falling")
 
 
 @pytest.mark.parametrize("rows,D,out", [(1, 256, BF16), (3, 64, F32), (40, 128, BF16),
@@ -291,9 +300,10 @@ def test_attention_strides_and_unowned_rows(pq, dev, rows, D, out):
     qs[2:2 + T] = q
     hold = torch.full((6, T + 4, D + 8), 7.0, dtype=out, device=dev)
     o = hold[:, :, :D].transpose(0, 1)                  # heads outside tokens
-    got = pq.pq1_paged_attention(qs, cache, table, cu + 2, kv, max_q=rows, max_kv=rows + 77, out=o)
-    assert got is o
-    s.check(o[2:2 + T], where="strided")
+    for stated in STATED:
+        got = pq.pq1_paged_attention(qs, cache, table, cu + 2, kv, max_q=rows, max_kv=stated, out=o)
+        assert got is o
+        s.check(o[2:2 + T], where="strided")
     assert bool((hold[:, :2] == 7).all()) and bool((hold[:, T + 2:] == 7).all())
     assert bool((hold[:, :, D:] == 7).all())
 
@@ -304,6 +314,8 @@ def test_attention_sizes_beyond_the_hints(pq, dev, rows):
     s.check(s.run(), where="true hints")
     s.check(s.run(max_q=1, max_kv=1), where="hints too small")
     s.check(s.run(max_q=4 * rows, max_kv=9000), where="hints too large")
+    s.check(s.run(max_q=1, max_kv=10 ** 6), where="one hint too small, one too large")
+    s.check(s.run(max_q=4 * rows, max_kv=1), where="one hint too large, one too small")
 
 
 @pytest.mark.parametrize("page", [16, 64])
@@ -322,41 +334,44 @@ def test_attention_odd_values(pq, dev, rows, D, page):
             s.k[0][kv - 1, 0, 1] = float("nan")
         s.fill()
         for out in (BF16, F32):
-            s.check(s.run(out_dtype=out), where=f"odd {what}")
+            for stated in STATED:
+                s.check(s.run(max_kv=stated, out_dtype=out), where=f"odd {what}, stated {stated}")
     s = Batch(pq, dev, [rows], [kv], 1, 2, D, page, BF16, seed=4)
     s.v[0][20, 0, 3] = float("inf")                           # before every row's window
     s.k[0][21] = float("nan")
     s.fill()
-    s.check(s.run(window=90), window=90, where="outside the window")
+    for stated in STATED:
+        s.check(s.run(max_kv=stated, window=90), window=90, where="outside the window")
 
 
+@pytest.mark.parametrize("stated", STATED)
 @pytest.mark.parametrize("page", [8, 32, 128])
 @pytest.mark.parametrize("rows", [1, 6, 90])
-def test_attention_bad_pages(pq, dev, rows, page):
+def test_attention_bad_pages(pq, dev, rows, page, stated):
     """A page outside the cache makes NaN of the rows that see it, and
     nothing else is read; a page that a window has left may be anything."""
     kv = rows + 300
     s = Batch(pq, dev, [rows, 3], [kv, 40], 2, 4, 64, page, BF16)
-    want = s.run()
+    want = s.run(max_kv=stated)
     last = (kv - 1) // page
     good = int(s.table[0, last])
     for bad in (-1, s.pages, 2 ** 31 - 1, -2 ** 31):
         s.table[0, last] = bad
-        got = s.run()
+        got = s.run(max_kv=stated)
         sees = torch.arange(rows) + kv - rows >= last * page
         assert bool(torch.isnan(got[:rows].cpu()[sees]).all())
         assert not bool(torch.isnan(got[:rows].cpu()[~sees]).any())
         assert torch.equal(got[rows:], want[rows:])
         s.table[0, last] = good
     short = s.pq.pq1_paged_attention(*(a if i != 2 else a[:, :last].contiguous()
-                                       for i, a in enumerate(s.args())), max_q=rows, max_kv=kv)
+                                       for i, a in enumerate(s.args())), max_q=rows, max_kv=stated)
     assert torch.equal(torch.isnan(short[:rows]).all(-1).all(-1).cpu(),
                        torch.arange(rows) + kv - rows >= last * page)
-    want = s.run(window=100)
+    want = s.run(max_kv=stated, window=100)
     left = (kv - rows + 1 - 100) // page                     # pages no window reaches
     if left > 0:
         s.table[0, :left] = -1
-        assert torch.equal(s.run(window=100), want)
+        assert torch.equal(s.run(max_kv=stated, window=100), want)
 
 
 def test_attention_lengths_outside_their_range(pq, dev):
@@ -378,14 +393,14 @@ def test_attention_far_into_a_large_cache(pq, dev):
     pages = (1 << 32) // (Hk * page * D) + 40
     kc = torch.empty((pages, Hk, page, D), dtype=BF16, device=dev)
     vc = torch.empty((pages, Hk, page, D), dtype=BF16, device=dev)
-    for rows in (1, 40):
+    for rows, stated in ((1, 200), (40, 200), (40, 10 ** 6)):
         s = Batch(pq, dev, [rows], [200], Hk, 2, D, page, BF16)
         far = torch.tensor([pages - 1, 3, pages - 7, pages // 2 + 1])
         for i, p in enumerate(far.tolist()):
             kc[p], vc[p] = s.cache.k[int(s.table[0, i])], s.cache.v[int(s.table[0, i])]
         s.table[0, :4] = far.to(torch.int32)
         s.cache = pq.KVCache(kc, vc)
-        s.check(s.run(), where="large cache")
+        s.check(s.run(max_kv=stated), where="large cache")
     new = torch.randn(2, Hk, D, dtype=BF16, device=dev)
     slots = torch.tensor([pages * page - 1, (pages - 2) * page + 5], device=dev)
     pq.pq1_kv_append(s.cache, new, new, slots)
