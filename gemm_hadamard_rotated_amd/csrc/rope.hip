@@ -4,10 +4,15 @@
 // Pair i of a head, (x0, x1), is turned by theta = p[a(i)] * freqs[i]:
 //   y0 = x0 cos(theta) - x1 sin(theta),  y1 = x1 cos(theta) + x0 sin(theta).
 // The angle depends on the token and the pair but not on the head, so a
-// workgroup first puts (cos, sin) of its tokens' pairs into LDS and then
-// streams all heads of those tokens past the table.  The angle is taken in
+// workgroup, with its loads in flight, puts (cos, sin) of its tokens' pairs into
+// LDS, and all heads of those tokens use that table.  The angle is taken in
 // turns in fp64 (p * f / 2 pi) and reduced there; only the reduced turn, at
 // most half, is narrowed to fp32 for the sine and cosine.
+//
+// Bound: the memory traffic; a few tokens by the launch.  8190 tokens of 24
+// heads of 256 bf16: 201 MB in 48 us, 4.2 TB/s (a large copy reaches 5.1);
+// 4001 tokens of 24 + 4 + 4 heads, fp32 in, appended: 42 us, 4.7 TB/s; one token
+// 3 us, as an empty kernel.
 #include "attn_device.h"
 #include "attn_internal.h"
 
@@ -28,10 +33,11 @@ struct Dims {
   int rot_units;       // units of a head that hold pairs; the rest are copies
 };
 
-// A unit is VEC pairs of a head (VEC elements from each of two places: VEC
-// low and VEC high elements, or 2 VEC neighbours), VEC copied elements of a
-// head's tail, or 8 elements of a value head.
-template <typename TI, typename TO, int VEC, bool APPEND>
+// A unit is VEC elements at each of two places of a head: the two halves of
+// VEC pairs (or 2 VEC neighbours that are VEC pairs), or 2 VEC elements to
+// copy (the last of a head may have but one place).  A thread takes U units
+// and has all their loads in flight before the workgroup makes its table.
+template <typename TI, typename TO, int VEC, int U, bool APPEND>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
   __shared__ float2 table[kTable];
   const uint32_t group = dm.parts.div(blockIdx.x);
@@ -39,6 +45,57 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
   const int64_t t0 = static_cast<int64_t>(group) * dm.tokens;
   const int nt = static_cast<int>(a.T - t0 < dm.tokens ? a.T - t0 : dm.tokens);
   const int half = a.rot >> 1;
+  const uint32_t total = static_cast<uint32_t>(nt) * dm.per_token.d;
+
+  TO* dst[U];
+  int at0[U], at1[U], angle[U];  // angle: of the unit's first pair, -1 to copy
+  float e[U][VEC], g[U][VEC];
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    dst[k] = nullptr;
+    const uint32_t u = (part * U + k) * kThreads + threadIdx.x;
+    if (u >= total) continue;
+    const uint32_t tl = dm.per_token.div(u);
+    uint32_t w = u - tl * dm.per_token.d;
+    const int64_t t = t0 + tl;
+    const TI* src;
+    bool value = false;
+    const uint32_t nx = a.Hx * dm.per_head.d, nk = a.Hk * dm.per_head.d;
+    if (APPEND && w >= nx) {
+      const int64_t slot = a.slots[t];
+      if (slot < 0 || slot >= a.slot_count) continue;
+      const int64_t page = slot >> a.page_shift;
+      const int64_t row = slot - (page << a.page_shift);
+      w -= nx;
+      value = w >= nk;
+      if (value) w -= nk;
+      const FastDiv& by = value ? dm.per_value : dm.per_head;
+      const uint32_t h = by.div(w);
+      w -= h * by.d;
+      src = value ? static_cast<const TI*>(a.v) + t * a.v_ts + h * a.v_hs
+                  : static_cast<const TI*>(a.k) + t * a.k_ts + h * a.k_hs;
+      dst[k] = static_cast<TO*>(value ? a.v_cache : a.k_cache) +
+               (((page * a.Hk + h) << a.page_shift) + row) * a.D;
+    } else {
+      const uint32_t h = dm.per_head.div(w);
+      w -= h * dm.per_head.d;
+      src = static_cast<const TI*>(a.x) + t * a.x_ts + h * a.x_hs;
+      dst[k] = static_cast<TO*>(a.y) + t * a.y_ts + h * a.y_hs;
+    }
+    const int p0 = w * VEC;
+    if (!value && static_cast<int>(w) < dm.rot_units) {
+      angle[k] = tl * half + p0;
+      at0[k] = a.adjacent ? 2 * p0 : p0;
+      at1[k] = a.adjacent ? 2 * p0 + VEC : p0 + half;
+    } else {
+      angle[k] = -1;
+      at0[k] = value ? 2 * p0 : a.rot + 2 * (p0 - dm.rot_units * VEC);
+      at1[k] = at0[k] + VEC;
+      if (at1[k] >= a.D) at1[k] = at0[k];  // the same place twice
+    }
+    load_wide(src + at0[k], e[k]);
+    load_wide(src + at1[k], g[k]);
+  }
 
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int t = static_cast<int>(dm.pairs.div(i));
@@ -60,60 +117,15 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
   }
   __syncthreads();
 
-  const uint32_t total = static_cast<uint32_t>(nt) * dm.per_token.d;
-  for (uint32_t u = part * kThreads + threadIdx.x; u < total; u += dm.parts.d * kThreads) {
-    const uint32_t tl = dm.per_token.div(u);
-    uint32_t w = u - tl * dm.per_token.d;
-    const int64_t t = t0 + tl;
-    const TI* src;
-    TO* dst;
-    int64_t slot = 0;
-    if (APPEND) {
-      const uint32_t nx = a.Hx * dm.per_head.d, nk = a.Hk * dm.per_head.d;
-      if (w >= nx) {
-        slot = a.slots[t];
-        if (slot < 0 || slot >= a.slot_count) continue;
-        const int64_t page = slot >> a.page_shift;
-        const int64_t row = slot - (page << a.page_shift);
-        if (w >= nx + nk) {  // a value: 8 elements, rounded
-          w -= nx + nk;
-          const uint32_t h = dm.per_value.div(w), c = w - h * dm.per_value.d;
-          float e[8];
-          load_wide(static_cast<const TI*>(a.v) + t * a.v_ts + h * a.v_hs + 8 * c, e);
-          store_wide(static_cast<TO*>(a.v_cache) +
-                         (((page * a.Hk + h) << a.page_shift) + row) * a.D + 8 * c,
-                     e);
-          continue;
-        }
-        w -= nx;
-        const uint32_t h = dm.per_head.div(w);
-        w -= h * dm.per_head.d;
-        src = static_cast<const TI*>(a.k) + t * a.k_ts + h * a.k_hs;
-        dst = static_cast<TO*>(a.k_cache) + (((page * a.Hk + h) << a.page_shift) + row) * a.D;
-      } else {
-        const uint32_t h = dm.per_head.div(w);
-        w -= h * dm.per_head.d;
-        src = static_cast<const TI*>(a.x) + t * a.x_ts + h * a.x_hs;
-        dst = static_cast<TO*>(a.y) + t * a.y_ts + h * a.y_hs;
-      }
-    } else {
-      const uint32_t h = dm.per_head.div(w);
-      w -= h * dm.per_head.d;
-      src = static_cast<const TI*>(a.x) + t * a.x_ts + h * a.x_hs;
-      dst = static_cast<TO*>(a.y) + t * a.y_ts + h * a.y_hs;
-    }
-    if (static_cast<int>(w) < dm.rot_units) {
-      const int p0 = w * VEC;
-      const float2* cs = table + tl * half + p0;
-      const int at0 = a.adjacent ? 2 * p0 : p0;
-      const int at1 = a.adjacent ? 2 * p0 + VEC : p0 + half;
-      float e[VEC], g[VEC], y0[VEC], y1[VEC];
-      load_wide(src + at0, e);
-      load_wide(src + at1, g);
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    if (dst[k] == nullptr) continue;
+    if (angle[k] >= 0) {
+      const float2* cs = table + angle[k];
       if (a.adjacent) {
         float z[2 * VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) z[i] = e[i], z[VEC + i] = g[i];
+        for (int i = 0; i < VEC; ++i) z[i] = e[k][i], z[VEC + i] = g[k][i];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           const float2 r = cs[i];
@@ -122,24 +134,39 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
           z[2 * i + 1] = x1 * r.x + x0 * r.y;
         }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) y0[i] = z[i], y1[i] = z[VEC + i];
+        for (int i = 0; i < VEC; ++i) e[k][i] = z[i], g[k][i] = z[VEC + i];
       } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           const float2 r = cs[i];
-          y0[i] = e[i] * r.x - g[i] * r.y;
-          y1[i] = g[i] * r.x + e[i] * r.y;
+          const float x0 = e[k][i], x1 = g[k][i];
+          e[k][i] = x0 * r.x - x1 * r.y;
+          g[k][i] = x1 * r.x + x0 * r.y;
         }
       }
-      store_wide(dst + at0, y0);
-      store_wide(dst + at1, y1);
-    } else {
-      const int at = a.rot + (static_cast<int>(w) - dm.rot_units) * VEC;
-      float e[VEC];
-      load_wide(src + at, e);
-      store_wide(dst + at, e);
     }
+    store_wide(dst[k] + at0[k], e[k]);
+    store_wide(dst[k] + at1[k], g[k]);
   }
+}
+
+template <typename TI, typename TO, int VEC, int U, bool APPEND>
+hipError_t launch_units(const RopeArgs& a, Dims dm, hipStream_t s) {
+  // A group's tokens fill its workgroup, or one token is shared by several;
+  // the group's table has to fit.
+  const int half = a.rot / 2;
+  const int64_t per_token = dm.per_token.d;
+  int64_t tokens = U * kThreads / per_token;
+  if (tokens * half > kTable) tokens = kTable / half;
+  if (tokens < 1) tokens = 1;
+  dm.tokens = static_cast<int>(tokens);
+  const int64_t parts = (tokens * per_token + U * kThreads - 1) / (U * kThreads);
+  dm.parts = FastDiv(static_cast<uint32_t>(parts));
+  const int64_t groups = (a.T + tokens - 1) / tokens;
+  if (groups * parts >= (int64_t{1} << 32) / kThreads) return hipErrorInvalidConfiguration;
+  rope_kernel<TI, TO, VEC, U, APPEND>
+      <<<dim3(static_cast<uint32_t>(groups * parts)), kThreads, 0, s>>>(a, dm);
+  return hipGetLastError();
 }
 
 template <typename TI, typename TO, int VEC, bool APPEND>
@@ -147,30 +174,18 @@ hipError_t launch_vec(const RopeArgs& a, hipStream_t s) {
   Dims dm;
   const int half = a.rot / 2;
   dm.rot_units = half / VEC;
-  const int per_head = dm.rot_units + (a.D - a.rot) / VEC;
-  const int per_value = a.D / 8;
+  const int per_head = dm.rot_units + (a.D - a.rot + 2 * VEC - 1) / (2 * VEC);
+  const int per_value = (a.D + 2 * VEC - 1) / (2 * VEC);
   const int64_t per_token = static_cast<int64_t>(a.Hx + (APPEND ? a.Hk : 0)) * per_head +
                             (APPEND ? static_cast<int64_t>(a.Hk) * per_value : 0);
   dm.per_head = FastDiv(per_head);
   dm.per_value = FastDiv(per_value);
   dm.per_token = FastDiv(static_cast<uint32_t>(per_token));
   dm.pairs = FastDiv(half > 0 ? half : 1);
-  // A few units for each thread where there are enough to fill the device,
-  // one otherwise; a group's table has to fit.
-  const int64_t total = a.T * per_token;
-  const int64_t want = total / (256 * 8 * kThreads);  // units a thread would get
-  const int64_t each = want < 1 ? 1 : want > 8 ? 8 : want;
-  int64_t tokens = each * kThreads / per_token;
-  if (tokens * half > kTable) tokens = kTable / half;
-  if (tokens < 1) tokens = 1;
-  dm.tokens = static_cast<int>(tokens);
-  const int64_t per_group = tokens * per_token;
-  const int64_t parts = (per_group + each * kThreads - 1) / (each * kThreads);
-  dm.parts = FastDiv(static_cast<uint32_t>(parts));
-  const int64_t groups = (a.T + tokens - 1) / tokens;
-  rope_kernel<TI, TO, VEC, APPEND>
-      <<<dim3(static_cast<uint32_t>(groups * parts)), kThreads, 0, s>>>(a, dm);
-  return hipGetLastError();
+  // One unit a thread until those fill the device, then two (four: 50, eight:
+  // 55, a loop over the units 66 us where two take 48).
+  return a.T * per_token < 256 * 8 * kThreads ? launch_units<TI, TO, VEC, 1, APPEND>(a, dm, s)
+                                              : launch_units<TI, TO, VEC, 2, APPEND>(a, dm, s);
 }
 
 template <typename TI, typename TO, bool APPEND>
@@ -188,9 +203,13 @@ hipError_t launch_in(const RopeArgs& a, int out_dtype, hipStream_t s) {
   const bool append = a.slots != nullptr;
   switch (out_dtype) {
     case PQ1_BF16:
-      return append ? launch_types<TI, bf16, true>(a, s) : launch_types<TI, bf16, false>(a, s);
+      if constexpr (!__is_same(TI, f16))
+        if (append) return launch_types<TI, bf16, true>(a, s);
+      return launch_types<TI, bf16, false>(a, s);
     case PQ1_F16:
-      return append ? launch_types<TI, f16, true>(a, s) : launch_types<TI, f16, false>(a, s);
+      if constexpr (!__is_same(TI, bf16))
+        if (append) return launch_types<TI, f16, true>(a, s);
+      return launch_types<TI, f16, false>(a, s);
     default:
       return launch_types<TI, float, false>(a, s);
   }
