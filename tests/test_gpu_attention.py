@@ -450,3 +450,107 @@ def test_attention_layer_on_a_side_stream_and_in_a_graph(pq, dev):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, step()), f"replay {i}"
+
+
+def test_example_layer(pq, dev):
+    """Chunks and single tokens give what the whole prompt gives.  Both round
+    activations, probabilities and queries to bf16 (2^-8 each; single tokens do
+    not round the projection's input), so outputs differ by a few times 2^-8 of
+    their size."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                                    "examples"))
+    import attention_layer as ex
+    layer = ex.AttentionLayer(hidden=1024, heads=4, kv_heads=2, dim=256, pages=40, page_size=16)
+    x = torch.randn(150, 1024, device=dev, generator=torch.Generator(device=dev).manual_seed(1))
+    whole = ex.run(layer, x, range(10), [150])
+    parts = ex.run(layer, x, range(30, 20, -1), [64, 1, 50, 33, 1, 1])
+    size = whole.double().pow(2).mean().sqrt()
+    assert float((parts - whole).double().pow(2).mean().sqrt()) <= 8 * 2 ** -8 * float(size)
+    # the layer against its 64-bit form, from the projection's output on
+    D, seq = 256, ex.Sequence(layer, range(10))
+    a = seq.extend(150)
+    qkv = layer._project(x, layer.qkv)
+    q, k, v = (qkv[:, i * D:j * D].unflatten(1, (j - i, D)) for i, j in ((0, 4), (4, 6), (6, 8)))
+    qr = pq.pq1_kv_append(layer.cache, k, v, a["slots"], positions=a["positions"], rope=layer.rope,
+                          q=q)
+    o = pq.pq1_paged_attention(qr, layer.cache, a["table"], a["cu_q"], a["kv_len"], 150, 150,
+                               out_dtype=F32)
+    f = layer.rope.freqs.cpu()
+    kr, _ = ref.rotate(k.cpu(), a["positions"].cpu(), f, (11, 11, 10), "halves", True)
+    e, w, spread = ref.attention(qr.cpu(), kr.to(BF16), v.cpu().to(BF16), D ** -0.5, True, 0)
+    # a key may round to the other neighbour: two bf16 steps of every score
+    b = ref.attention_bound(e, w, spread, 150, 0.0, D, BF16, F32) + 2 * w * 2 ** -7 * spread
+    check(o, e, b, "example")
+
+
+def test_binding_refusals(pq, dev):
+    """Raised before anything is launched."""
+    s = Batch(pq, dev, [2], [40], 2, 2, 64, 16, BF16)
+    q, cache, table, cu, kv = s.args()
+    att = lambda *a, **k: pq.pq1_paged_attention(*a, max_q=2, max_kv=40, **k)
+    with pytest.raises(TypeError):
+        att(q.float(), cache, table, cu, kv)
+    with pytest.raises(ValueError):
+        att(q[..., :32].contiguous(), cache, table, cu, kv)
+    with pytest.raises(ValueError):
+        att(q.transpose(1, 2).contiguous().transpose(1, 2), cache, table, cu, kv)
+    with pytest.raises(TypeError):
+        att(q, cache, table.long(), cu, kv)
+    with pytest.raises(ValueError):
+        att(q, cache, table, cu[:1], kv)
+    with pytest.raises(ValueError):
+        att(q, cache, table[:, ::2], cu, kv)
+    with pytest.raises(ValueError):
+        att(q, cache, table.cpu(), cu, kv)
+    with pytest.raises(TypeError):
+        att(q, cache, table, cu, kv, out_dtype=F16)
+    with pytest.raises(ValueError):
+        att(q, cache, table, cu, kv, out=torch.empty(3, 4, 64, dtype=BF16, device=dev))
+    with pytest.raises(pq.Pq1Error):
+        att(q[:, :3].contiguous(), cache, table, cu, kv)          # 3 heads over 2
+    with pytest.raises(pq.Pq1Error):
+        att(q, cache, table, cu, kv, scale=-1.0)
+    with pytest.raises(pq.Pq1Error):
+        att(q, cache, table, cu, kv, causal=False, window=3)
+    with pytest.raises(pq.Pq1Error):
+        att(q, cache, table, cu, kv, out=q)
+    odd = pq.KVCache(torch.zeros(2, 1, 24, 64, dtype=BF16, device=dev),
+                     torch.zeros(2, 1, 24, 64, dtype=BF16, device=dev))
+    with pytest.raises(pq.Pq1Error):
+        att(q, odd, table, cu, kv)                                # pages of 24
+    rope = pq.Rope(32, (8, 8), freqs=pq.rope_frequencies(32, device=dev))
+    pos = torch.zeros(2, 2, dtype=torch.int32, device=dev)
+    with pytest.raises(ValueError):
+        pq.pq1_rope(q, pos[:1], rope)
+    with pytest.raises(TypeError):
+        pq.pq1_rope(q, pos.long(), rope)
+    with pytest.raises(pq.Pq1Error):
+        pq.pq1_rope(q[..., :24].contiguous(), pos, rope)          # 32 elements of 24
+    for bad in (dict(rot=31), dict(rot=32, sections=(8, 9)), dict(rot=32, sections=(4,) * 5),
+                dict(rot=32, pairing="thirds")):
+        with pytest.raises(pq.Pq1Error):
+            pq.Rope(freqs=pq.rope_frequencies(bad["rot"], device=dev), **bad)
+    new, slots = torch.zeros(2, 2, 64, dtype=BF16, device=dev), torch.arange(2, device=dev)
+    with pytest.raises(ValueError):
+        pq.pq1_kv_append(cache, new, new, slots[:1])
+    with pytest.raises(TypeError):
+        pq.pq1_kv_append(cache, new, new.float(), slots)
+    with pytest.raises(ValueError):
+        pq.pq1_kv_append(cache, new, new, slots, rope=rope)
+    with pytest.raises(ValueError):
+        pq.pq1_kv_append(cache, new, new, slots, q_out=new)
+    with pytest.raises(ValueError):
+        pq.pq1_kv_append(cache, new[:, :1], new[:, :1], slots)
+
+
+def test_empty_calls(pq, dev):
+    s = Batch(pq, dev, [0, 0], [5, 0], 2, 2, 64, 16, BF16)
+    assert s.run().shape == (0, 4, 64)
+    rope = pq.Rope(32, freqs=pq.rope_frequencies(32, device=dev))
+    none = torch.empty(0, 2, 64, dtype=BF16, device=dev)
+    pos = torch.empty(0, dtype=torch.int32, device=dev)
+    assert pq.pq1_rope(none, pos, rope).shape == (0, 2, 64)
+    got = pq.pq1_kv_append(s.cache, none, none, pos.long(), positions=pos, rope=rope, q=none)
+    assert got.shape == (0, 2, 64)
