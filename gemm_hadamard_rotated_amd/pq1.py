@@ -673,7 +673,9 @@ _PAIRINGS = {"halves": PQ1_ROPE_HALVES, "adjacent": PQ1_ROPE_ADJACENT}
 # layer), so their path through Python is kept short: addresses go as plain
 # integers, the stream comes from torch's raw accessor (0.1 us; a Stream object
 # takes 2), and what a Rope or a KVCache can check is checked when it is made.
+# A result is made like its input, in plain order (1.3 us; by its sizes 2.1).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_plain = torch.contiguous_format
 _current_device = torch._C._cuda_getDevice
 
 
@@ -798,7 +800,7 @@ def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
         dt = x.dtype if out_dtype is None else out_dtype
         if dt not in _TYPE_CODE:
             raise TypeError(f"out_dtype must be in {_FLOATS}")
-        out = torch.empty(size, dtype=dt, device=dev)
+        out = torch.empty_like(x, dtype=dt, memory_format=_plain)
         yv = Pq1Heads(out.data_ptr(), _TYPE_CODE[dt], H * D, D)
     else:
         if out_dtype is not None and out.dtype != out_dtype:
@@ -870,7 +872,7 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
         if size[0] != T or size[2] != cache.dim:
             raise ValueError(f"q has shape {tuple(size)}, expected {(T, Hq, cache.dim)}")
         if q_out is None:
-            q_out = torch.empty(size, dtype=dt, device=dev)
+            q_out = torch.empty_like(q, dtype=dt, memory_format=_plain)
             ov = Pq1Heads(q_out.data_ptr(), _TYPE_CODE[dt], Hq * cache.dim, cache.dim)
         else:
             ov = _need_heads(q_out, "q_out", (dt,), dev, size)
@@ -932,7 +934,7 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
             if out_dtype != dt and out_dtype != torch.float32:
                 raise TypeError(f"out_dtype must be {dt} or torch.float32")
             dt = out_dtype
-        out = torch.empty(size, dtype=dt, device=dev)
+        out = torch.empty_like(q, dtype=dt, memory_format=_plain)
         ov = Pq1Heads(out.data_ptr(), _TYPE_CODE[dt], Hq * D, D)
     else:
         if out_dtype is not None and out.dtype != out_dtype:
