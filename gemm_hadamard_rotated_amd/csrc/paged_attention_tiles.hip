@@ -13,16 +13,17 @@
 // reads that transpose 4 keys x 16 dimensions do.  So P never leaves its lane,
 // and a row's maximum and sum need one exchange between the halves of a wave.
 //
-// Bound: the matrix instructions.  8192 rows of 8 cache heads against 7168
-// keys take 471 us at D = 256 (1021 TFLOP/s), 282 us at 128 (850) and 198 us at
-// 64 (609); a large library product reaches 1263 TFLOP/s on the same card, and
-// this loop with its reads, copies and softmax taken out 1366 at D = 256.
-// What was measured on the way: the scores and outputs of a wave fill its
-// registers (two waves a SIMD; 64 rows a wave spills, one wave a SIMD of 64
-// rows is slower, 759 against 505 us for 2048 tokens after 6144 at D = 256);
-// page numbers from LDS and no other load in the loop, so that copies stay in
-// flight over the barrier (478 -> 458 us); waves of one SIMD set half a tile
-// apart: no gain (the compiler's own order overlaps them as well).
+// Bound: the matrix instructions and, for small D, the softmax between them.
+// 8192 rows of 8 cache heads against 7168 keys take 444 us at D = 256 (1084
+// TFLOP/s), 260 us at 128 (924) and 191 us at 64 (631); a large library product
+// reaches 1263 TFLOP/s on the same card.
+// What was measured on the way (D = 128 of the above unless said): 64 rows a
+// wave, one wave a SIMD: slower (759 against 505 us for 2048 tokens after 6144
+// at D = 256); page numbers from LDS and no load waited for in the loop, so
+// that copies stay in flight over the barrier: 285 -> 265 us; priority for the
+// wave that computes scores: 265 -> 260 us (D = 256: 460 -> 444); waves of one
+// SIMD set half a tile apart: 274 us; a barrier every second tile: 267 us;
+// tiles of pages of 64 keys or more copied as one run: no gain.
 #include "attn_tiles.h"
 
 namespace pq1 {
@@ -225,6 +226,8 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
         return D == 256 ? n / 2 + 8 * (n % 2) : n / EB;
       };
       const int kx = here(kat);
+      // first in line for the matrix pipe: the other wave of the SIMD does its softmax
+      __builtin_amdgcn_s_setprio(1);
       U4 kf[AHEAD];
       auto read = [&](int n) {
         const int e = EB == 2 ? n % 2 : 0, d = step(n);
@@ -269,6 +272,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
                                                 : sc[e][i];
           }
       }
+      __builtin_amdgcn_s_setprio(0);
       float top = sc[0][0];
 #pragma unroll
       for (int e = 0; e < EB; ++e)
@@ -352,6 +356,10 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
       find_pages(first + 2 * KT, page);
       wait_copies<2 * COPIES>();
       __syncthreads();
+      // The rows' loads end here: a wait for them inside the loop would be one
+      // for the copies as well.
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) asm volatile("" : "+v"(q[d]));
       int now = 0, then = 2 * TILE;
 #pragma unroll 1
       for (int j0 = first; j0 < end; j0 += KT) {
