@@ -318,14 +318,25 @@ def test_attention_sizes_beyond_the_hints(pq, dev, rows):
     s.check(s.run(max_q=4 * rows, max_kv=1), where="one hint too large, one too small")
 
 
-@pytest.mark.parametrize("page", [16, 64])
-@pytest.mark.parametrize("rows,D", [(1, 64), (4, 128), (30, 256), (120, 128)])
-def test_attention_odd_values(pq, dev, rows, D, page):
+@pytest.mark.parametrize("D", [64, 256])
+def test_attention_more_pages_than_a_workgroup_holds(pq, dev, D):
+    """Pages of one key: the page numbers of a part are taken in pieces."""
+    s = Batch(pq, dev, [20, 17], [9000, 4100], 1, 2, D, 1, BF16)
+    for stated in STATED + [2 * 10 ** 6, 10 ** 9]:
+        s.check(s.run(max_kv=stated), where=f"stated {stated}")
+    s = Batch(pq, dev, [33], [9000], 1, 2, D, 1, BF16, seed=1)
+    for stated in (2 * 10 ** 6, 10 ** 9):
+        s.check(s.run(max_kv=stated, window=6000), window=6000, where=f"stated {stated}")
+
+
+@pytest.mark.parametrize("page,dt", [(16, BF16), (64, F16), (4, BF16)])
+@pytest.mark.parametrize("rows,D", [(1, 64), (4, 128), (30, 256), (120, 128), (70, 64)])
+def test_attention_odd_values(pq, dev, rows, D, page, dt):
     """Infinities and NaN in values reach the rows that see them, and no
     others; in keys likewise."""
     kv = rows + 150
     for what in ("value", "key"):
-        s = Batch(pq, dev, [rows], [kv], 1, 2, D, page, BF16, seed=3)
+        s = Batch(pq, dev, [rows], [kv], 1, 2, D, page, dt, seed=3)
         if what == "value":
             s.v[0][kv - 1, 0, 5] = float("nan")              # only the last token sees it
             s.v[0][kv - 1, 0, 6] = float("inf")
@@ -333,10 +344,10 @@ def test_attention_odd_values(pq, dev, rows, D, page):
         else:
             s.k[0][kv - 1, 0, 1] = float("nan")
         s.fill()
-        for out in (BF16, F32):
+        for out in (dt, F32):
             for stated in STATED:
                 s.check(s.run(max_kv=stated, out_dtype=out), where=f"odd {what}, stated {stated}")
-    s = Batch(pq, dev, [rows], [kv], 1, 2, D, page, BF16, seed=4)
+    s = Batch(pq, dev, [rows], [kv], 1, 2, D, page, dt, seed=4)
     s.v[0][20, 0, 3] = float("inf")                           # before every row's window
     s.k[0][21] = float("nan")
     s.fill()
