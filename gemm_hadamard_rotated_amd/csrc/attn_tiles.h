@@ -170,6 +170,21 @@ __device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) 
   }
 }
 
+// l + both probabilities of a pair: the sum of what the product takes, so that
+// a rounding of the largest ones is divided out again.
+template <typename T>
+__device__ __forceinline__ float add_pair(uint32_t pair, float l) {
+  if constexpr (__is_same(T, bf16)) {
+    using B2 = __attribute__((ext_vector_type(2))) __bf16;
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(B2, pair),
+                                           __builtin_bit_cast(B2, 0x3f803f80u), l, false);
+  } else {
+    using H2 = __attribute__((ext_vector_type(2))) _Float16;
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(H2, pair), __builtin_bit_cast(H2, 0x3c003c00u),
+                                  l, false);
+  }
+}
+
 // Bits 15 and 31 of the result say which of two elements is an infinity or NaN
 // (an exponent of ones carries into its sign's place; the other bits are odds
 // and ends).

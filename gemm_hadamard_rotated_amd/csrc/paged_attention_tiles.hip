@@ -14,8 +14,8 @@
 // and a row's maximum and sum need one exchange between the halves of a wave.
 //
 // Bound: the matrix instructions and, for small D, the softmax between them.
-// 8192 rows of 8 cache heads against 7168 keys take 444 us at D = 256 (1084
-// TFLOP/s), 260 us at 128 (924) and 191 us at 64 (631); a large library product
+// 8192 rows of 8 cache heads against 7168 keys take 439 us at D = 256 (1096
+// TFLOP/s), 260 us at 128 (925) and 187 us at 64 (644); a large library product
 // reaches 1263 TFLOP/s on the same card.
 // What was measured on the way (D = 128 of the above unless said): 64 rows a
 // wave, one wave a SIMD: slower (759 against 505 us for 2048 tokens after 6144
@@ -23,7 +23,9 @@
 // that copies stay in flight over the barrier: 285 -> 265 us; priority for the
 // wave that computes scores: 265 -> 260 us (D = 256: 460 -> 444); waves of one
 // SIMD set half a tile apart: 274 us; a barrier every second tile: 267 us;
-// tiles of pages of 64 keys or more copied as one run: no gain.
+// tiles of pages of 64 keys or more copied as one run: no gain; 32-bit offsets
+// for the copies and sums of probabilities in pairs: 264 -> 260 us (ragged
+// prompts 386 -> 377).
 #include "attn_tiles.h"
 
 namespace pq1 {
@@ -70,12 +72,21 @@ __device__ __forceinline__ int here(int x) {
 // same for the whole wave).  Written as an instruction because the compiler
 // would wait for all copies in flight before each read of LDS that it cannot
 // tell apart from them; here the wait is wait_copies and a barrier.
+__device__ __forceinline__ uint32_t lds_at(const char* p) {
+  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p)));
+}
 __device__ __forceinline__ void copy16(const char* from, char* to) {
-  const uint32_t at = static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)to));
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
-               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(from)
+               : "s"(lds_at(to)), "v"(from)
+               : "m0");
+}
+// The same from a place that the whole wave shares, plus a lane's offset.
+__device__ __forceinline__ void copy16(const char* from, uint32_t offset, char* to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %1"
+               :
+               : "s"(lds_at(to)), "s"(from), "v"(offset)
                : "m0");
 }
 // Waits until at most N copies of this wave are in flight.
@@ -92,7 +103,7 @@ struct TileGrid {
 
 constexpr int kTileWaves = kTileRows / 32;
 
-template <typename T, typename TO, int D>
+template <typename T, typename TO, int D, bool WIDE>
 __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, TileGrid tg,
                                                                     float* part_o,
                                                                     float2* part_ml) {
@@ -159,19 +170,18 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
     float m = kNegInf, l = 0.0f;
     bool odd_values = false;  // infinities or NaN were taken out of V
 
-    // Pages of keys first .. end - 1 are in LDS; -1: no page of the cache.
+    // Pages of keys first .. end - 1 are in LDS: the number, -1 for no page of
+    // the cache; or, where K and V take less than 4 GB each, the byte at which
+    // the page's rows of this head begin, one more than page 0's for none.
     // Keys past the last take its page, so that every address lies in the
     // cache.  A lane looks up the rows that it copies, a tile ahead.
     int first = 0, end = 0;
     auto page_at = [&](int j) { return page_lds[(j >> a.page_shift) - (first >> a.page_shift)]; };
+    auto is_gone = [](int entry) { return WIDE ? entry < 0 : (entry & 1) != 0; };
     auto up_to_end = [&](int j) { return j < end ? j : end - 1; };
     auto gone_of = [&](int j0) {  // keys of a tile on no page of the cache
-      const uint64_t bits = __ballot(page_at(up_to_end(j0 + lane)) < 0);
+      const uint64_t bits = __ballot(is_gone(page_at(up_to_end(j0 + lane))));
       return KT == 64 ? bits : bits & 0xffffffffu;
-    };
-    auto row_of = [&](int page, int j) {
-      return ((static_cast<int64_t>(page < 0 ? 0 : page) * a.Hk + h) << a.page_shift) +
-             (j & page_mask);
     };
     const int crow = wave * (COPIES * CROWS) + lane / PIECES;  // the row of copy 0
     auto find_pages = [&](int j0, int (&page)[COPIES]) {
@@ -181,14 +191,24 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
     auto copy = [&](const int (&page)[COPIES], int j0, char* kb, char* vb) {
       const int r = here(crow), piece = here(lane) % PIECES;
       const int kp = 16 * (piece ^ k_bits<D>(r)), vp = 16 * (piece ^ v_bits<D>(r));
+      const char* k = static_cast<const char*>(a.k_cache);
+      const char* v = static_cast<const char*>(a.v_cache);
 #pragma unroll
       for (int c = 0; c < COPIES; ++c) {
-        const int64_t at = row_of(page[c], up_to_end(j0 + r + c * CROWS)) * ROWB;
+        const int in_page = up_to_end(j0 + r + c * CROWS) & page_mask;
+        const int kc = kp ^ 16 * k_bits<D>(c * CROWS), vc = vp ^ 16 * v_bits<D>(c * CROWS);
         const int to = (wave * COPIES + c) * 1024;
-        copy16(static_cast<const char*>(a.k_cache) + at + (kp ^ 16 * k_bits<D>(c * CROWS)),
-               kb + to);
-        copy16(static_cast<const char*>(a.v_cache) + at + (vp ^ 16 * v_bits<D>(c * CROWS)),
-               vb + to);
+        if constexpr (WIDE) {
+          const int64_t at =
+              (((static_cast<int64_t>(page[c] < 0 ? 0 : page[c]) * a.Hk + h) << a.page_shift) +
+               in_page) * ROWB;
+          copy16(k + at + kc, kb + to);
+          copy16(v + at + vc, vb + to);
+        } else {
+          const uint32_t at = (static_cast<uint32_t>(page[c]) & ~1u) + in_page * ROWB;
+          copy16(k, at + kc, kb + to);
+          copy16(v, at + vc, vb + to);
+        }
       }
     };
     // Values no row sees become zero, and where there are infinities or NaN
@@ -297,9 +317,13 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           p[i] = __builtin_amdgcn_exp2f(fmaf(sc[st / 2][8 * (st % 2) + i], a.scale_log2, shift));
-          l += p[i];
+          if constexpr (NP > 1) l += p[i];
         }
         split_probs<T, NP>(p, pr[st]);
+        if constexpr (NP == 1) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) l = add_pair<T>(pr[st][0][w], l);
+        }
       }
       const int vx = here(vat);
       U4 vf[AHEAD];
@@ -344,7 +368,11 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
       for (int p = p0 + static_cast<int>(threadIdx.x); p <= p1; p += 64 * kTileWaves) {
         const int page = p < a.max_pages ? table[p] : -1;
         const bool bad = page < 0 || page >= a.pages;
-        page_lds[p - p0] = bad ? -1 : page;
+        if constexpr (WIDE)
+          page_lds[p - p0] = bad ? -1 : page;
+        else
+          page_lds[p - p0] = (((static_cast<uint32_t>(bad ? 0 : page) * a.Hk + h) << a.page_shift) *
+                              ROWB) | bad;
         lost |= bad;
       }
       const bool any_gone = __syncthreads_or(lost);
@@ -426,7 +454,13 @@ hipError_t launch_tiles(const AttnPlan& plan, const AttnArgs& a, void* workspace
   float2* part_ml =
       reinterpret_cast<float2*>(part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
   const dim3 grid(static_cast<uint32_t>(a.B * a.Hk * plan.row_tiles * plan.nsplit));
-  many_rows_kernel<T, TO, D><<<grid, 64 * kTileWaves, 0, s>>>(a, tg, part_o, part_ml);
+  // 32-bit offsets into K and V where they reach (D = 64 of the above: 193 us
+  // with 64-bit ones, 186 with these)
+  const bool wide = ((static_cast<uint64_t>(a.pages) * a.Hk << a.page_shift) * 2 * D) >> 32 != 0;
+  if (wide)
+    many_rows_kernel<T, TO, D, true><<<grid, 64 * kTileWaves, 0, s>>>(a, tg, part_o, part_ml);
+  else
+    many_rows_kernel<T, TO, D, false><<<grid, 64 * kTileWaves, 0, s>>>(a, tg, part_o, part_ml);
   return hipGetLastError();
 }
 
