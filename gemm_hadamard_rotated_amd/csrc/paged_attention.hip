@@ -23,9 +23,9 @@ namespace {
 // V, and picking one dimension of the 8 keys is a byte permute of registers.
 //
 // Bound: reading the cache; a call of one token by its fixed cost.  One token
-// at 131071 keys (4 cache heads, D = 256): 103 us, 5.2 TB/s (a large copy
+// at 131071 keys (4 cache heads, D = 256): 99 us, 5.4 TB/s (a large copy
 // reaches 5.1, a cached one more); 64 tokens at 200 to 8000 keys: 232 us, 4.9
-// TB/s; one token at 701 keys: 8 us for this kernel and 4.6 for the join, where
+// TB/s; one token at 701 keys: 8 us for this kernel and 4.2 for the join, where
 // an empty kernel takes 3.  What paid: as many workgroups as CUs (twice as
 // many: 109 and 239 us), divisions by multiplication, lengths and page numbers
 // through the scalar cache, runs of 16 keys as buffers whose end cuts off the
@@ -381,21 +381,26 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void few_rows_kernel
   }
 }
 
-// Joins the parts of every row: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
-// One wave per row, D / 64 dimensions a lane.
-template <typename TO, int D>
+// Joins the parts of every row: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,
+// eight parts at a time with all their loads in flight, under a running
+// maximum.  WPR waves share a row (each takes every WPR-th eight), D / 64
+// dimensions a lane.
+template <typename TO, int D, int WPR>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, FewGrid fg, int tile_rows,
                                                    int tokens, const float* part_o,
                                                    const float2* part_ml) {
-  constexpr int N = D / 64;
+  constexpr int N = D / 64, RPW = 4 / WPR, BATCH = 8;
+  __shared__ float sum_o[WPR > 1 ? 4 : 1][D];
+  __shared__ float sum_m[4], sum_l[4];
   const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int Hq = a.Hk * a.G;
-  const uint32_t heads4 = (Hq + 3) / 4;
-  const uint32_t id = blockIdx.x / heads4;
-  const int hq = (blockIdx.x - id * heads4) * 4 + (threadIdx.x >> 6);
+  const uint32_t groups = (Hq + RPW - 1) / RPW;
+  const uint32_t id = blockIdx.x / groups;
+  const int hq = (blockIdx.x - id * groups) * RPW + wave / WPR;
   const uint32_t b = id / static_cast<uint32_t>(tokens);
   const Seq s = load_seq(a, b);
-  if (hq >= Hq) return;
+  if (hq >= Hq) return;  // (whole workgroups where waves share a row)
   const int64_t stride = a.T * Hq;
   const int hq_in = hq - static_cast<int>(a.by_G.div(hq)) * a.G;
   for (int i = id - b * tokens; i < s.n; i += tokens) {
@@ -406,24 +411,68 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, FewGrid fg, int t
     int lo, hi;
     visible(a, s, i, &lo, &hi);
     const int64_t row = (s.q0 + i) * Hq + hq;
-    float top = kNegInf;
-    for (int p = lane; p < count; p += 64) top = fmaxf(top, part_ml[p * stride + row].x);
+    float acc[N] = {}, l = 0.0f, top = kNegInf;
+    for (int p0 = wave % WPR * BATCH; p0 < count; p0 += WPR * BATCH) {
+      float2 ml[BATCH];
+      float x[BATCH][N], up = top;
 #pragma unroll
-    for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-    float acc[N] = {}, l = 0.0f;
-#pragma unroll 8
-    for (int p = 0; p < count; ++p) {
-      const float2 ml = part_ml[p * stride + row];
-      const float w = ml.x == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
-      float x[N];
-      load_wide(part_o + (p * stride + row) * D + N * lane, x);
-      l += w * ml.y;
+      for (int k = 0; k < BATCH; ++k) {
+        const int p = p0 + k < count ? p0 + k : count - 1;
+        ml[k] = part_ml[p * stride + row];
+        load_wide(part_o + (p * stride + row) * D + N * lane, x[k]);
+      }
 #pragma unroll
-      for (int n = 0; n < N; ++n) acc[n] += w * x[n];
+      for (int k = 1; k < BATCH; ++k) {  // past the last part: nothing
+        const bool part = p0 + k < count;
+        ml[k].x = part ? ml[k].x : kNegInf;
+        ml[k].y = part ? ml[k].y : 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[k][n] = part ? x[k][n] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) up = fmaxf(up, ml[k].x);
+      const float keep = top == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(top - up);
+      top = up;
+      l *= keep;
+#pragma unroll
+      for (int n = 0; n < N; ++n) acc[n] *= keep;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        // a part without a finite score still hands on its NaN
+        const float w = ml[k].x == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ml[k].x - top);
+        l += w * ml[k].y;
+#pragma unroll
+        for (int n = 0; n < N; ++n) acc[n] += w * x[k][n];
+      }
     }
+    if constexpr (WPR > 1) {
+      if (lane == 0) sum_m[wave] = top, sum_l[wave] = l;
+      store_wide(&sum_o[wave][N * lane], acc);
+      __syncthreads();
+      if (wave == 0) {
+        top = kNegInf;
 #pragma unroll
-    for (int n = 0; n < N; ++n) acc[n] = hi > lo ? acc[n] / l : 0.0f;
-    store_wide(static_cast<TO*>(a.out) + (s.q0 + i) * a.o_ts + hq * a.o_hs + N * lane, acc);
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, sum_m[w]);
+        l = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) acc[n] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = sum_m[w] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(sum_m[w] - top);
+          float x[N];
+          load_wide(&sum_o[w][N * lane], x);
+          l += f * sum_l[w];
+#pragma unroll
+          for (int n = 0; n < N; ++n) acc[n] += f * x[n];
+        }
+      }
+    }
+    if (wave % WPR == 0) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) acc[n] = hi > lo ? acc[n] / l : 0.0f;
+      store_wide(static_cast<TO*>(a.out) + (s.q0 + i) * a.o_ts + hq * a.o_hs + N * lane, acc);
+    }
+    if constexpr (WPR > 1) __syncthreads();
   }
 }
 
@@ -448,18 +497,27 @@ hipError_t launch_few(const AttnPlan& plan, const AttnArgs& a, void* workspace, 
   return hipGetLastError();
 }
 
-template <typename TO, int D>
-hipError_t launch_join(const AttnPlan& plan, const AttnArgs& a, void* workspace, hipStream_t s) {
+template <typename TO, int D, int WPR>
+hipError_t launch_join_waves(const AttnPlan& plan, const AttnArgs& a, void* workspace,
+                             hipStream_t s) {
   const FewGrid fg = grid_of(plan, a);
   const float* part_o = static_cast<const float*>(workspace);
   const float2* part_ml = reinterpret_cast<const float2*>(
       part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
-  const int64_t heads4 = (a.Hk * a.G + 3) / 4;
-  const int64_t most = ((int64_t{1} << 24) - 1) / (a.B * heads4);  // below 2^32 threads
+  constexpr int RPW = 4 / WPR;
+  const int64_t groups = (a.Hk * a.G + RPW - 1) / RPW;
+  const int64_t most = ((int64_t{1} << 24) - 1) / (a.B * groups);  // below 2^32 threads
   const int64_t tokens = plan.tokens < most ? plan.tokens : most;
-  join_kernel<TO, D><<<dim3(static_cast<uint32_t>(a.B * tokens * heads4)), 256, 0, s>>>(
+  join_kernel<TO, D, WPR><<<dim3(static_cast<uint32_t>(a.B * tokens * groups)), 256, 0, s>>>(
       a, fg, plan.tile_rows, static_cast<int>(tokens), part_o, part_ml);
   return hipGetLastError();
+}
+
+template <typename TO, int D>
+hipError_t launch_join(const AttnPlan& plan, const AttnArgs& a, void* workspace, hipStream_t s) {
+  // four waves to a row where there are several batches (64 parts: 9.1 -> 5.4 us)
+  return plan.nsplit > 8 ? launch_join_waves<TO, D, 4>(plan, a, workspace, s)
+                         : launch_join_waves<TO, D, 1>(plan, a, workspace, s);
 }
 
 template <typename T, typename TO, int D>
