@@ -679,51 +679,52 @@ _plain = torch.contiguous_format
 _current_device = torch._C._cuda_getDevice
 
 
-def _need_heads(t: torch.Tensor, name: str, dtypes, dev=None, shape=None) -> Pq1Heads:
-    """A [tokens][heads][dim] tensor with contiguous head vectors, as the
-    library's view of it."""
+def _refuse(t, name: str, dtypes, dev, shape=None):
+    """Raise what is wrong with an argument."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (no CPU path exists)")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    dt = t.dtype
-    if dt not in dtypes:
-        raise TypeError(f"{name} must have dtype in {dtypes}, got {dt}")
-    size = t.shape
-    if shape is not None and size != shape:
-        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
-    if len(size) != 3:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if shape is not None:
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{name} must be contiguous")
+    if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D, [tokens][heads][dim]")
-    ts, hs, ds = t.stride()
-    if ds != 1 and size[2] != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    raise ValueError(f"{name}: the elements of a head must be contiguous")
+
+
+def _need_heads(t: torch.Tensor, name: str, dtypes, dev=None):
+    """A [tokens][heads][dim] tensor with contiguous head vectors: the
+    library's view of it, and its shape."""
+    try:
+        dt, size = t.dtype, t.shape
+        ts, hs, ds = t.stride()
+        if dt not in dtypes or (not t.is_cuda if dev is None else t.device != dev) or (
+                ds != 1 and size[2] != 1):
+            _refuse(t, name, dtypes, dev)
+    except (AttributeError, ValueError):  # no tensor, or not of three axes
+        _refuse(t, name, dtypes, dev)
     # the stride of an axis of length one says nothing
     return Pq1Heads(t.data_ptr(), _TYPE_CODE[dt], ts if size[0] > 1 else 0,
-                    hs if size[1] > 1 else 0)
+                    hs if size[1] > 1 else 0), size
 
 
 def _need_vector(t: torch.Tensor, name: str, dtype: torch.dtype, dev, shape) -> int:
     """The address of a contiguous tensor of this type and shape on dev."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU (no CPU path exists)")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev \
+            or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, (dtype,), dev, shape)
     return t.data_ptr()
 
 
-def _need_shape(t: torch.Tensor, name: str, shape):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _same(size, expected, name: str):
+    if size != expected:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(expected)}")
 
 
 def _launch(dev: torch.device, where: str, fn, *args):
@@ -777,10 +778,9 @@ class Rope:
     def _need_positions(self, positions: torch.Tensor, T: int, dev) -> int:
         if self._device != dev:
             raise ValueError(f"the rotation's freqs are on {self._device}, expected {dev}")
-        shape = (self.axes, T)
         if self.axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1:
-            shape = (T,)
-        return _need_vector(positions, "positions", torch.int32, dev, shape)
+            return _need_vector(positions, "positions", torch.int32, dev, (T,))
+        return _need_vector(positions, "positions", torch.int32, dev, (self.axes, T))
 
 
 def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
@@ -790,10 +790,10 @@ def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
 
     x may be a slice (contiguous heads); out may be x itself.  inverse=True
     turns back, which is also the gradient of the forward call."""
-    xv = _need_heads(x, "x", _FLOATS)
+    xv, size = _need_heads(x, "x", _FLOATS)
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
-    dev, size = x.device, x.shape
+    dev = x.device
     T, H, D = size
     pos = rope._need_positions(positions, T, dev)
     if out is None:
@@ -805,7 +805,8 @@ def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
-        yv = _need_heads(out, "out", _FLOATS, dev, size)
+        yv, out_size = _need_heads(out, "out", _FLOATS, dev)
+        _same(out_size, size, "out")
     _launch(dev, "pq1_rope", (_lib or load_library()).pq1_rope, xv, yv, pos, rope._freqs,
             rope._spec[1 if inverse else 0], T, H, D)
     return out
@@ -820,10 +821,11 @@ class KVCache:
         _need(v, "v", (k.dtype,), k.device)
         if k.dim() != 4:
             raise ValueError("k must be 4-D, [pages][heads][page_size][dim]")
-        _need_shape(v, "v", k.shape)
+        _same(v.shape, k.shape, "v")
         self.k, self.v = k, v
         self.pages, self.heads, self.page_size, self.dim = (int(n) for n in k.shape)
         self.dtype, self.device = k.dtype, k.device
+        self._inputs = (torch.float32, k.dtype)
         self._struct = Pq1KvCache(k.data_ptr(), v.data_ptr(), _TYPE_CODE[k.dtype],
                                   self.page_size, self.pages, self.heads, self.dim)
 
@@ -847,13 +849,12 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     dev, dt = cache.device, cache.dtype
-    kv = _need_heads(k, "k", (torch.float32, dt), dev)
-    T = k.shape[0]
-    shape = (T, cache.heads, cache.dim)
-    if k.shape != shape:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected {shape}")
+    kv, size = _need_heads(k, "k", cache._inputs, dev)
+    T = size[0]
+    _same(size, (T, cache.heads, cache.dim), "k")
     kind = (k.dtype,)
-    vv = _need_heads(v, "v", kind, dev, shape)
+    vv, v_size = _need_heads(v, "v", kind, dev)
+    _same(v_size, size, "v")
     at = _need_vector(slots, "slots", torch.int64, dev, (T,))
     spec = pos = freqs = None
     if rope is not None:
@@ -866,16 +867,15 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
     qv = ov = None
     Hq = 0
     if q is not None:
-        qv = _need_heads(q, "q", kind, dev)
-        size = q.shape
+        qv, size = _need_heads(q, "q", kind, dev)
         Hq = size[1]
-        if size[0] != T or size[2] != cache.dim:
-            raise ValueError(f"q has shape {tuple(size)}, expected {(T, Hq, cache.dim)}")
+        _same(size, (T, Hq, cache.dim), "q")
         if q_out is None:
             q_out = torch.empty_like(q, dtype=dt, memory_format=_plain)
             ov = Pq1Heads(q_out.data_ptr(), _TYPE_CODE[dt], Hq * cache.dim, cache.dim)
         else:
-            ov = _need_heads(q_out, "q_out", (dt,), dev, size)
+            ov, out_size = _need_heads(q_out, "q_out", (dt,), dev)
+            _same(out_size, size, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
     _launch(dev, "pq1_kv_append", (_lib or load_library()).pq1_kv_append, kv, vv, at, qv, ov, Hq,
@@ -916,8 +916,7 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     dev, dt = cache.device, cache.dtype
-    qv = _need_heads(q, "q", (dt,), dev)
-    size = q.shape
+    qv, size = _need_heads(q, "q", (dt,), dev)
     T, Hq, D = size
     if D != cache.dim:
         raise ValueError(f"q has shape {tuple(size)}, expected {(T, Hq, cache.dim)}")
@@ -939,7 +938,8 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
-        ov = _need_heads(out, "out", (dt, torch.float32), dev, size)
+        ov, out_size = _need_heads(out, "out", (dt, torch.float32), dev)
+        _same(out_size, size, "out")
     lib = _lib or load_library()
     max_q, max_kv = int(max_q), int(max_kv)
     need = lib.pq1_paged_attention_workspace_bytes(B, T, Hq, cache.heads, D, max_q, max_kv)
