@@ -883,22 +883,23 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
     return q_out
 
 
-# Attention workspaces, one per (device, stream), grown on demand; kept apart
-# from the GEMV's, whose counter region must stay as its calls leave it.
+# Attention workspaces, one per (device, stream) and grown on demand: (tensor,
+# address, bytes).  Kept apart from the GEMV's, whose counter region must stay
+# as its calls leave it.
 _attn_ws = {}
+_NO_WS = (None, None, 0)
 
 
-def attention_workspace(need: int, device: torch.device) -> torch.Tensor:
-    key = (device.index, _raw_stream(device.index))
+def _grow_attention_workspace(key, need: int, device: torch.device):
     with _ws_lock:
-        ws = _attn_ws.get(key)
-        if ws is None or ws.numel() < need:
-            if ws is not None:
+        old = _attn_ws.get(key, _NO_WS)
+        if old[2] < need:
+            if old[0] is not None:
                 # a graph captured earlier may still hold the old buffer's address
-                _ws_retired.append(ws)
-            ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=device)
-            _attn_ws[key] = ws
-        return ws
+                _ws_retired.append(old[0])
+            t = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=device)
+            old = _attn_ws[key] = (t, t.data_ptr(), t.numel())
+        return old
 
 
 def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
@@ -941,11 +942,30 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
         ov, out_size = _need_heads(out, "out", (dt, torch.float32), dev)
         _same(out_size, size, "out")
     lib = _lib or load_library()
-    max_q, max_kv = int(max_q), int(max_kv)
-    need = lib.pq1_paged_attention_workspace_bytes(B, T, Hq, cache.heads, D, max_q, max_kv)
-    ws = attention_workspace(need, dev).data_ptr() if need else None
-    _launch(dev, "pq1_paged_attention", lib.pq1_paged_attention, qv, ov, cache._struct, table,
-            max_pages, cu, lens, B, T, Hq, max_q, max_kv,
-            D ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window), ws,
-            need)
+    args = (qv, ov, cache._struct, table, max_pages, cu, lens, B, T, Hq, int(max_q), int(max_kv),
+            D ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window))
+    if _current_device() == dev.index:
+        _attend(lib, dev, cache.heads, args)
+    else:
+        with torch.cuda.device(dev):
+            _attend(lib, dev, cache.heads, args)
     return out
+
+
+def _attend(lib, dev, heads: int, args) -> None:
+    """The call with the stream's present workspace; only if the library
+    refuses that is the size asked for (0.5 us a call)."""
+    stream = _raw_stream(dev.index)
+    key = (dev.index, stream)
+    ws = _attn_ws.get(key, _NO_WS)
+    code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
+    if code == PQ1_OK:
+        return
+    if code in (1, 8):  # PQ1_ERR_NULL, PQ1_ERR_ARG: perhaps no workspace yet, or too small a one
+        B, T, Hq, max_q, max_kv = args[7:12]
+        need = lib.pq1_paged_attention_workspace_bytes(B, T, Hq, heads, args[2].dim, max_q, max_kv)
+        if need > ws[2]:
+            ws = _grow_attention_workspace(key, need, dev)
+            code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
+    if code != PQ1_OK:
+        _check(code, "pq1_paged_attention")
