@@ -31,12 +31,35 @@ struct Dims {
   FastDiv pairs;       // rot / 2 (1 without rotation)
   int tokens;          // tokens of a group
   int rot_units;       // units of a head that hold pairs; the rest are copies
+  int tail;            // elements of a tail's unit
 };
 
-// A unit is VEC elements at each of two places of a head: the two halves of
-// VEC pairs (or 2 VEC neighbours that are VEC pairs), or 2 VEC elements to
-// copy (the last of a head may have but one place).  A thread takes U units
-// and has all their loads in flight before the workgroup makes its table.
+// A unit is some elements at each of two places of a head: the two halves of
+// VEC pairs (or 2 VEC neighbours that are VEC pairs), 16 elements of a value,
+// or a piece of a head's tail: 2 VEC elements where VEC is 4 or 8 (then every
+// lane does the same); else 16, which begin at any pair of elements, or 2 of a
+// tail of less than 8.  A last piece may overlap the one before or be one place
+// twice.  A thread takes U units and has all their loads in flight before the
+// workgroup makes its table.
+template <int W, int ALIGN = 16, typename T>
+__device__ __forceinline__ void load_first(const T* p, float (&o)[8]) {
+  struct alignas(sizeof(T) * W < ALIGN ? sizeof(T) * W : ALIGN) Piece {
+    T e[W];
+  };
+  const Piece x = *reinterpret_cast<const Piece*>(p);
+#pragma unroll
+  for (int i = 0; i < W; ++i) o[i] = static_cast<float>(x.e[i]);
+}
+template <int W, int ALIGN = 16, typename T>
+__device__ __forceinline__ void store_first(T* p, const float (&v)[8]) {
+  struct alignas(sizeof(T) * W < ALIGN ? sizeof(T) * W : ALIGN) Piece {
+    T e[W];
+  };
+  Piece x;
+#pragma unroll
+  for (int i = 0; i < W; ++i) x.e[i] = static_cast<T>(v[i]);
+  *reinterpret_cast<Piece*>(p) = x;
+}
 template <typename TI, typename TO, int VEC, int U, bool APPEND>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
   __shared__ float2 table[kTable];
@@ -48,8 +71,9 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
   const uint32_t total = static_cast<uint32_t>(nt) * dm.per_token.d;
 
   TO* dst[U];
-  int at0[U], at1[U], angle[U];  // angle: of the unit's first pair, -1 to copy
-  float e[U][VEC], g[U][VEC];
+  // angle: of the unit's first pair; -1: a copy of a tail, -2: of a value
+  int at0[U], at1[U], angle[U];
+  float e[U][8], g[U][8];
 #pragma unroll
   for (int k = 0; k < U; ++k) {
     dst[k] = nullptr;
@@ -82,19 +106,39 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
       src = static_cast<const TI*>(a.x) + t * a.x_ts + h * a.x_hs;
       dst[k] = static_cast<TO*>(a.y) + t * a.y_ts + h * a.y_hs;
     }
-    const int p0 = w * VEC;
-    if (!value && static_cast<int>(w) < dm.rot_units) {
+    int step;
+    if (value) {
+      angle[k] = -2;
+      at0[k] = 16 * w;
+      step = 8;
+    } else if (static_cast<int>(w) < dm.rot_units) {
+      const int p0 = w * VEC;
       angle[k] = tl * half + p0;
       at0[k] = a.adjacent ? 2 * p0 : p0;
-      at1[k] = a.adjacent ? 2 * p0 + VEC : p0 + half;
+      step = a.adjacent ? VEC : half;
     } else {
       angle[k] = -1;
-      at0[k] = value ? 2 * p0 : a.rot + 2 * (p0 - dm.rot_units * VEC);
-      at1[k] = at0[k] + VEC;
-      if (at1[k] >= a.D) at1[k] = at0[k];  // the same place twice
+      at0[k] = a.rot + dm.tail * (static_cast<int>(w) - dm.rot_units);
+      step = VEC >= 4 ? VEC : dm.tail == 16 ? 8 : 0;
     }
-    load_wide(src + at0[k], e[k]);
-    load_wide(src + at1[k], g[k]);
+    at1[k] = at0[k] + step;
+    if (VEC < 4 && angle[k] == -1 && dm.tail == 16) {
+      at0[k] = at0[k] < a.D - 8 ? at0[k] : a.D - 8;
+      at1[k] = at1[k] < a.D - 8 ? at1[k] : a.D - 8;
+    }
+    if (at1[k] >= a.D) at1[k] = at0[k];
+    if (angle[k] >= 0 || (VEC >= 4 && angle[k] == -1) || VEC == 8) {
+      load_first<VEC>(src + at0[k], e[k]);
+      load_first<VEC>(src + at1[k], g[k]);
+    } else if (APPEND && angle[k] == -2) {
+      load_first<8>(src + at0[k], e[k]);
+      load_first<8>(src + at1[k], g[k]);
+    } else if (VEC < 4 && dm.tail == 16) {
+      load_first<8, 2 * sizeof(TI)>(src + at0[k], e[k]);
+      load_first<8, 2 * sizeof(TI)>(src + at1[k], g[k]);
+    } else if (VEC < 4) {
+      load_first<2>(src + at0[k], e[k]);
+    }
   }
 
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
@@ -145,8 +189,18 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
         }
       }
     }
-    store_wide(dst[k] + at0[k], e[k]);
-    store_wide(dst[k] + at1[k], g[k]);
+    if (angle[k] >= 0 || (VEC >= 4 && angle[k] == -1) || VEC == 8) {
+      store_first<VEC>(dst[k] + at0[k], e[k]);
+      store_first<VEC>(dst[k] + at1[k], g[k]);
+    } else if (APPEND && angle[k] == -2) {
+      store_first<8>(dst[k] + at0[k], e[k]);
+      store_first<8>(dst[k] + at1[k], g[k]);
+    } else if (VEC < 4 && dm.tail == 16) {
+      store_first<8, 2 * sizeof(TO)>(dst[k] + at0[k], e[k]);
+      store_first<8, 2 * sizeof(TO)>(dst[k] + at1[k], g[k]);
+    } else if (VEC < 4) {
+      store_first<2>(dst[k] + at0[k], e[k]);
+    }
   }
 }
 
@@ -174,8 +228,10 @@ hipError_t launch_vec(const RopeArgs& a, hipStream_t s) {
   Dims dm;
   const int half = a.rot / 2;
   dm.rot_units = half / VEC;
-  const int per_head = dm.rot_units + (a.D - a.rot + 2 * VEC - 1) / (2 * VEC);
-  const int per_value = (a.D + 2 * VEC - 1) / (2 * VEC);
+  const int tail = a.D - a.rot;
+  dm.tail = VEC >= 4 ? 2 * VEC : tail >= 8 ? 16 : 2;
+  const int per_head = dm.rot_units + (tail + dm.tail - 1) / dm.tail;
+  const int per_value = (a.D + 15) / 16;
   const int64_t per_token = static_cast<int64_t>(a.Hx + (APPEND ? a.Hk : 0)) * per_head +
                             (APPEND ? static_cast<int64_t>(a.Hk) * per_value : 0);
   dm.per_head = FastDiv(per_head);
@@ -190,11 +246,13 @@ hipError_t launch_vec(const RopeArgs& a, hipStream_t s) {
 
 template <typename TI, typename TO, bool APPEND>
 hipError_t launch_types(const RopeArgs& a, hipStream_t s) {
-  // 16-byte accesses where the pairs of a head come in eights, 8-byte ones
-  // (for two-byte types) in fours, else single elements
+  // 16-byte accesses (for two-byte types) where the pairs of a head come in
+  // eights, shorter ones in fours, twos and ones (8000 tokens of 32 heads of 80,
+  // 20 of them rotated: 28 us; pairs and tails all by single elements 39 us)
   const int half = a.rot / 2;
   if (half % 8 == 0) return launch_vec<TI, TO, 8, APPEND>(a, s);
   if (half % 4 == 0) return launch_vec<TI, TO, 4, APPEND>(a, s);
+  if (half % 2 == 0) return launch_vec<TI, TO, 2, APPEND>(a, s);
   return launch_vec<TI, TO, 1, APPEND>(a, s);
 }
 

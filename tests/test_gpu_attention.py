@@ -47,6 +47,10 @@ ROPE = [
     (5, 1024, 16, 16, (0, 8), "halves", False, BF16, F32, 77),
     (70000, 1, 64, 32, (16,), "halves", False, BF16, BF16, 0),
     (3, 2, 1024, 1024, (512,), "adjacent", False, F32, BF16, 12),
+    (3000, 8, 72, 18, (9,), "halves", False, BF16, BF16, 0),      # tails at any pair of elements
+    (600, 3, 24, 18, (9,), "adjacent", False, F32, F16, 0),       # a tail of six
+    (5000, 8, 72, 36, (6, 6, 6), "halves", True, F16, F16, 0),
+    (5000, 4, 96, 24, (12,), "adjacent", False, BF16, F32, 0),
 ]
 
 
@@ -111,10 +115,22 @@ def test_rope_strided_in_place_and_gradient(pq, dev):
         assert abs(float(grad[t, h, d]) - diff) <= 1e-5
 
 
+@pytest.mark.parametrize("D,rot", [(72, 18), (80, 20), (24, 18), (40, 38), (96, 24), (128, 128)])
+@pytest.mark.parametrize("T", [3, 5000])
+def test_rope_in_place(pq, dev, T, D, rot):
+    x = torch.randn(T, 4, D, generator=torch.Generator().manual_seed(D)).to(BF16).to(dev)
+    pos = positions_of(T, 1, 0, 8).to(dev)
+    rope = pq.Rope(rot, freqs=pq.rope_frequencies(rot, device=dev))
+    want = pq.pq1_rope(x, pos, rope)
+    assert torch.equal(pq.pq1_rope(x, pos, rope, out=x), want)
+
+
 # ---------------------------------------------------------------------------
 # Append
 # ---------------------------------------------------------------------------
 APPEND = [
+    (4000, 4, 2, 80, 16, 20, (10,), "halves", False, BF16, BF16),
+    (900, 2, 3, 72, 4, 18, (9,), "adjacent", False, F32, F16),
     # T, Hk, G, D, page, rot, sections, pairing, interleaved, in, cache type
     (1, 4, 6, 256, 16, 64, (11, 11, 10), "halves", True, F32, BF16),
     (96, 8, 4, 128, 32, 128, (64,), "halves", False, F16, F16),
