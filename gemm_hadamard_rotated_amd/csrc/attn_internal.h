@@ -6,6 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "attn_plan.h"
 #include "pq1.h"
 
 namespace pq1 {
@@ -76,21 +77,6 @@ struct AttnArgs {
   int window = 0;
 };
 
-constexpr int kTileRows = 256;  // rows of a many-rows tile
-
-// How a call is cut into workgroups: a function of its sizes alone.
-struct AttnPlan {
-  int64_t tokens = 0;     // new tokens of the longest chunk
-  bool many = false;      // tiles of many rows (paged_attention_tiles.hip)
-  int tile_rows = 16;     // rows of a row tile
-  int64_t row_tiles = 0;  // row tiles of one (sequence, cache head)
-  int nsplit = 1;         // parts of the keys
-  int chunk = 0;          // keys of a part
-  size_t workspace_bytes = 0;
-  bool fits = false;      // the grid is launchable
-};
-AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_q,
-                        int64_t max_kv, int window = 0);
 hipError_t launch_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
                             void* workspace, hipStream_t s);
 hipError_t launch_attention(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,

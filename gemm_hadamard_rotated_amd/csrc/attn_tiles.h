@@ -11,8 +11,6 @@ namespace pq1 {
 
 constexpr float kNegInf = -__builtin_inff();
 
-constexpr int kMaxKeys = 0x7fff0000;  // of a sequence: key numbers plus a tile stay in 31 bits
-
 // What a workgroup needs to know of its sequence.
 struct Seq {
   int64_t q0;  // first row of q
