@@ -72,11 +72,13 @@ __device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int
   p.lo_max = lo1;
   p.hi_min = hi0;
   p.chunk = chunk;
-  // a cache longer than the caller said stretches the parts
+  // A cache longer than the caller said stretches the parts, to whole key tiles
+  // of either kernel as the plan's are: a part's last tile has no keys of the next.
   const int64_t room = static_cast<int64_t>(chunk) * nsplit;
   if (static_cast<int64_t>(p.hi) - p.start > room) {
+    constexpr uint32_t step = kKeys * kWaves;
     const uint32_t need = (static_cast<uint32_t>(p.hi - p.start) + nsplit - 1) / nsplit;
-    p.chunk = static_cast<int>((need + 31) & ~31u);
+    p.chunk = static_cast<int>((need + step - 1) / step * step);
   }
   return p;
 }

@@ -10,10 +10,50 @@ from test_gpu_attention import BF16, F16, F32, Batch, check, pq  # noqa: F401  (
 pytestmark = pytest.mark.gpu
 
 
+def attention_rows(q, k, v, scale, causal=True):
+    """ref.attention for finite inputs of which every row sees a key: all rows
+    of a head at once."""
+    q, k, v = q.double(), k.double(), v.double()
+    n, kv, G = q.shape[0], k.shape[0], q.shape[1] // k.shape[1]
+    o, weight, spread = torch.zeros_like(q), torch.zeros_like(q), 0.0
+    for h in range(q.shape[1]):
+        K, V = k[:, h // G], v[:, h // G]
+        e = (q[:, h] @ K.t()) * scale
+        spread = max(spread, float((q[:, h].abs() @ K.abs().t()).max()) * scale)
+        if causal:
+            e.masked_fill_(~torch.ones(n, kv, dtype=torch.bool).tril(kv - n), -float("inf"))
+        p = torch.softmax(e, dim=1)
+        o[:, h], weight[:, h] = p @ V, p @ V.abs()
+    return o, weight, spread
+
+
+def check_rows(s, got, where, causal=True):
+    """Batch.check of one sequence by attention_rows."""
+    e, w, spread = attention_rows(s.q, s.k[0], s.v[0], s.D ** -0.5, causal)
+    check(got, e, ref.attention_bound(e, w, spread, s.kvs[0], float(s.v[0].abs().max()), s.D,
+                                      s.dtype, got.dtype), where)
+
+
 @pytest.mark.parametrize("stated", [0x7fff0000, 0x7fffff01, 2 ** 31 - 1, 2 ** 62])
 @pytest.mark.parametrize("B,rows,G", [(64, 1, 6), (1, 150, 8), (2, 1, 2)])
 def test_longest_cache_stated_without_limit(pq, dev, B, rows, G, stated):
     """A caller that knows no limit states the largest number."""
     Hk = 4 if B > 1 else 32
-    s = Batch(pq, dev, [rows] * B, [9 + 3 * (b % 5) for b in range(B)], Hk, G, 64, 16, BF16)
-    s.check(s.run(max_kv=stated), where=f"stated {stated}")
+    kvs = [rows + 9 + 3 * (b % 5) for b in range(B)]
+    s = Batch(pq, dev, [rows] * B, kvs, Hk, G, 64, 16, BF16)
+    if B == 1:
+        check_rows(s, s.run(max_kv=stated), f"stated {stated}")
+    else:
+        s.check(s.run(max_kv=stated), where=f"stated {stated}")
+
+
+@pytest.mark.parametrize("kv", [2300, 2810, 3320])
+@pytest.mark.parametrize("D,G,dt", [(64, 4, BF16), (128, 4, F16), (128, 2, BF16), (256, 2, BF16)])
+def test_many_rows_in_parts_longer_than_stated(pq, dev, D, G, dt, kv):
+    """A prompt chunk whose keys are cut (8 parts of 256 keys are planned), on a
+    cache that has grown past the stated 2048 keys."""
+    s = Batch(pq, dev, [1024 // G], [kv], 8, G, D, 16, dt)
+    assert pq.load_library().pq1_paged_attention_workspace_bytes(
+        1, 1024 // G, 8 * G, 8, D, 1024 // G, 2048) == 8 * 1024 * 8 * (4 * D + 8)
+    check_rows(s, s.run(max_kv=2048), f"{kv} keys")
+    check_rows(s, s.run(max_kv=2048, causal=False), f"{kv} keys, all seen", causal=False)
