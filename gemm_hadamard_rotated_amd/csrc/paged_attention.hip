@@ -369,8 +369,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void few_rows_kernel
         }
       }
     }
+    // Read before the barrier: past it the next rows' sums and flags are written.
+    const bool put = !one_token && (odd_of[0] | odd_of[1] | odd_of[2] | odd_of[3]);
     __syncthreads();
-    if (!one_token && (odd_of[0] | odd_of[1] | odd_of[2] | odd_of[3])) {
+    if (put) {
       put_back<T, TO>(a, s, table, h, pt, k0, k1, kKeys, r0, ROWS, 64 * kWaves, split,
                       fg.nsplit > 1, part_o);
       __syncthreads();

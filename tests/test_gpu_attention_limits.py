@@ -57,3 +57,19 @@ def test_many_rows_in_parts_longer_than_stated(pq, dev, D, G, dt, kv):
         1, 1024 // G, 8 * G, 8, D, 1024 // G, 2048) == 8 * 1024 * 8 * (4 * D + 8)
     check_rows(s, s.run(max_kv=2048), f"{kv} keys")
     check_rows(s, s.run(max_kv=2048, causal=False), f"{kv} keys, all seen", causal=False)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("rows,kv,max_kv", [(40, 120, 1), (90, 90, 1), (70, 4000, 10 ** 6),
+                                            (33, 20, 1), (200, 3, 400)])
+def test_odd_values_in_chunks_longer_than_stated(pq, dev, rows, kv, max_kv, out):
+    """A workgroup that walks over several row tiles, infinities and NaN among
+    the values of some of them (and rows without a key)."""
+    s = Batch(pq, dev, [rows, 3], [kv, 50], 2, 4, 64, 16, BF16, seed=rows)
+    s.v[0][kv - 1, 0, 5] = float("nan")
+    s.v[0][kv - 1, 1, 6] = float("inf")
+    s.v[0][kv // 2, 0, 9] = float("-inf")
+    s.v[1][48, 1, 2] = float("inf")
+    s.fill()
+    for max_q in (1, 5):
+        s.check(s.run(max_q=max_q, max_kv=max_kv, out_dtype=out), where=f"stated {max_q} rows")
