@@ -125,12 +125,21 @@ constexpr float kUp = 8.0f, kLag = 6.0f;
 
 // A probability as NP two-byte numbers whose sum it is: one where the result
 // is rounded to that type anyway; for an fp32 result three bf16 or two f16,
-// which hold all 24 or 22 bits.  There each number is cut off, not rounded,
-// and what is left is kept above zero (by less than 2^-32 of the largest
-// probability), so that every part of a seen key's probability is positive and
-// an infinite value gives an infinity, not the difference of two.
+// which hold all 24 or 22 bits.  An infinite value times each of them has to
+// be an infinity, not NaN, so none of them is zero or negative.
+//   bf16: each number is cut off, and what is left is kept above zero (by less
+//   than 2^-90 of the largest probability).
+//   f16: the first is cut from slightly less than the probability, so that
+//   something is left for the second, which is rounded to nearest: together
+//   they are the probability to 22 bits or, where it is small, to the nearest
+//   2^-24 (2^-32 of the largest).  Below 1.75 of those the first is zero.
 template <typename T, typename TO>
 constexpr int kParts = sizeof(TO) == 2 ? 1 : __is_same(T, bf16) ? 3 : 2;
+
+// The sum of the probabilities is that of the parts, except where these hold
+// all of a probability.
+template <typename T, int NP>
+constexpr bool kSumParts = NP == 1 || __is_same(T, f16);
 
 template <typename T, int NP>
 __device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) {
@@ -139,8 +148,22 @@ __device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) 
 #pragma unroll
     for (int t = 0; t < 8; ++t) v[t] = static_cast<T>(p[t]);
     out[0] = __builtin_bit_cast(U4, v);
+  } else if constexpr (__is_same(T, f16)) {
+    Vec8<f16> rest;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float less[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) less[t] = fmaf(p[2 * w + t], 1.0f - 0x1p-23f, -0x1.8p-25f);
+      const auto c = __builtin_amdgcn_cvt_pkrtz(less[0], less[1]);
+      out[0][w] = __builtin_bit_cast(uint32_t, c);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        rest[2 * w + t] = static_cast<f16>(p[2 * w + t] - static_cast<float>(c[t]));
+    }
+    out[1] = __builtin_bit_cast(U4, rest);
   } else {
-    constexpr float least = __is_same(T, bf16) ? 0x1p-126f : 0x1p-24f;
+    constexpr float least = 0x1p-126f;
     float r[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) r[t] = p[t];
@@ -150,28 +173,18 @@ __device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) 
       for (int w = 0; w < 4; ++w) {
         float& x = r[2 * w];
         float& y = r[2 * w + 1];
-        float cx, cy;
-        if constexpr (__is_same(T, bf16)) {
-          const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
-          out[n][w] = __builtin_amdgcn_perm(uy, ux, 0x07060302u);
-          cx = __uint_as_float(ux & 0xffff0000u);
-          cy = __uint_as_float(uy & 0xffff0000u);
-        } else {
-          const auto c = __builtin_amdgcn_cvt_pkrtz(x, y);
-          out[n][w] = __builtin_bit_cast(uint32_t, c);
-          cx = static_cast<float>(c[0]);
-          cy = static_cast<float>(c[1]);
-        }
+        const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+        out[n][w] = __builtin_amdgcn_perm(uy, ux, 0x07060302u);
         if (n + 1 < NP) {
-          x = fmaxf(x - cx, fminf(p[2 * w], least));
-          y = fmaxf(y - cy, fminf(p[2 * w + 1], least));
+          x = fmaxf(x - __uint_as_float(ux & 0xffff0000u), fminf(p[2 * w], least));
+          y = fmaxf(y - __uint_as_float(uy & 0xffff0000u), fminf(p[2 * w + 1], least));
         }
       }
   }
 }
 
 // l + both probabilities of a pair: the sum of what the product takes, so that
-// a rounding of the largest ones is divided out again.
+// a rounding of the largest ones, or of many small ones, is divided out again.
 template <typename T>
 __device__ __forceinline__ float add_pair(uint32_t pair, float l) {
   if constexpr (__is_same(T, bf16)) {

@@ -283,12 +283,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void few_rows_kernel
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             p[4 * e + i] = __builtin_amdgcn_exp2f(fmaf(sc[rb][e][i], a.scale_log2, shift));
-            if constexpr (NP > 1) l[rb] += p[4 * e + i];
+            if constexpr (!kSumParts<T, NP>) l[rb] += p[4 * e + i];
           }
         split_probs<T, NP>(p, pr[rb]);
-        if constexpr (NP == 1) {
+        if constexpr (kSumParts<T, NP>) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) l[rb] = add_pair<T>(pr[rb][0][w], l[rb]);
+          for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) l[rb] = add_pair<T>(pr[rb][n][w], l[rb]);
         }
       }
 #pragma unroll

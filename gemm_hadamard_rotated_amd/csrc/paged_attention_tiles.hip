@@ -317,12 +317,14 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           p[i] = __builtin_amdgcn_exp2f(fmaf(sc[st / 2][8 * (st % 2) + i], a.scale_log2, shift));
-          if constexpr (NP > 1) l += p[i];
+          if constexpr (!kSumParts<T, NP>) l += p[i];
         }
         split_probs<T, NP>(p, pr[st]);
-        if constexpr (NP == 1) {
+        if constexpr (kSumParts<T, NP>) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) l = add_pair<T>(pr[st][0][w], l);
+          for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) l = add_pair<T>(pr[st][n][w], l);
         }
       }
       const int vx = here(vat);

@@ -73,3 +73,46 @@ def test_odd_values_in_chunks_longer_than_stated(pq, dev, rows, kv, max_kv, out)
     s.fill()
     for max_q in (1, 5):
         s.check(s.run(max_q=max_q, max_kv=max_kv, out_dtype=out), where=f"stated {max_q} rows")
+
+
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("B,rows,stated", [(1, 1, 1), (1, 20, 1), (130, 256, 8192)])
+def test_many_small_probabilities_of_f16(pq, dev, B, rows, stated, D):
+    """A first key of probability 1 and value 0, then n = 2^11 keys of 2^-20 and
+    value 1, all met by the same wave in one part (tiles of 32 keys, every
+    fourth; the keys between are far below); fp32 result n 2^-20 / (1 + n 2^-20).
+
+    An f16 probability is taken to the nearest 2^-32 of the largest, so each is
+    off by at most 2^-33: n 2^-33 in all.  The 32-bit sum of the probabilities
+    begins at the largest; a lane adds at most n / 2 times to it, each time off
+    by 2^-24 of it: n 2^-25 of the result, which is n 2^-20.  The numerator stays
+    below n 2^-20 (n / 16 additions, 2^-25 of that each), the exponential is good
+    to 2^-21, its argument to 2^-20, the result is rounded once."""
+    page, n = 256, 2 ** 11
+    kv = 4 * n
+    ln2 = torch.tensor(2.0, dtype=torch.float64).log()
+    hi = (-20 * ln2).to(F16)
+    lo = ((-20 * ln2 - hi.double()) * 2 ** 8).to(F16)
+    w = float(torch.exp(hi.double() + lo.double() * 2.0 ** -8))
+    assert abs(w * 2 ** 20 - 1) < 2.0 ** -18
+    small = torch.arange(kv, device=dev) // 32 % 4 == 0
+    small[0] = False
+    k = torch.zeros(kv, D, dtype=F16, device=dev)
+    k[:, 0] = torch.where(small, hi.to(dev), torch.tensor(-60000.0, dtype=F16, device=dev))
+    k[:, 1] = torch.where(small, lo.to(dev), torch.zeros((), dtype=F16, device=dev))
+    k[0] = 0
+    v = small.to(F16).unsqueeze(1).expand(kv, D)
+    paged = lambda x: x.reshape(kv // page, 1, page, D).contiguous()
+    q = torch.zeros(B * rows, 1, D, dtype=F16, device=dev)
+    q[..., 0], q[..., 1] = 1.0, 2.0 ** -8
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+    table = torch.arange(kv // page, dtype=torch.int32, device=dev).expand(B, -1).contiguous()
+    got = pq.pq1_paged_attention(q, pq.KVCache(paged(k), paged(v)), table,
+                                 i32([b * rows for b in range(B + 1)]), i32([kv] * B), max_q=rows,
+                                 max_kv=stated, scale=1.0, causal=False, out_dtype=F32).double()
+    share = (n - 1) * w
+    o = share / (1 + share)
+    bound = n * 2.0 ** -33 + o * (n * 2.0 ** -25 + n / 16 * 2.0 ** -25 + 2.0 ** -20 + 2.0 ** -21
+                                  + 2.0 ** -24)
+    worst = float((got - o).abs().max())
+    assert worst <= bound, f"off by {worst:.3e}, bound {bound:.3e}"
