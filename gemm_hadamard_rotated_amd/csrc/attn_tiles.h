@@ -118,17 +118,22 @@ __device__ __forceinline__ float sum_groups(float x) {
 }
 
 // Probabilities are carried times 2^kUp, which the division by their sum
-// takes out again: an f16 then holds those down to 2^-22 of the largest in
-// full.  The running maximum may lag behind by kLag (fewer rescalings of the
-// sums); 2^(kUp + kLag) is within f16.
-constexpr float kUp = 8.0f, kLag = 6.0f;
+// takes out again.  The running maximum may lag behind by kLag (fewer
+// rescalings of the sums).
+//   f16: up, so that it holds those down to 2^-22 of the largest in full;
+//   2^(kUp + kLag) is within f16.
+//   bf16: down, so that 2^(-kUp - kLag) values of any finite size, and any
+//   number of values below 2^111, sum up within fp32.
+template <typename T>
+constexpr float kUp = __is_same(T, bf16) ? -20.0f : 8.0f;
+constexpr float kLag = 6.0f;
 
 // A probability as NP two-byte numbers whose sum it is: one where the result
 // is rounded to that type anyway; for an fp32 result three bf16 or two f16,
 // which hold all 24 or 22 bits.  An infinite value times each of them has to
 // be an infinity, not NaN, so none of them is zero or negative.
 //   bf16: each number is cut off, and what is left is kept above zero (by less
-//   than 2^-90 of the largest probability).
+//   than 2^-100 of the largest probability).
 //   f16: the first is cut from slightly less than the probability, so that
 //   something is left for the second, which is rounded to nearest: together
 //   they are the probability to 22 bits or, where it is small, to the nearest

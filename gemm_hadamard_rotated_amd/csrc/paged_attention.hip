@@ -276,7 +276,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void few_rows_kernel
 #pragma unroll
           for (int n = 0; n < NO; ++n) o[rb][n] *= keep;
         }
-        const float shift = m[rb] == kNegInf ? 0.0f : kUp - m[rb];
+        const float shift = m[rb] == kNegInf ? 0.0f : kUp<T> - m[rb];
         float p[8];
 #pragma unroll
         for (int e = 0; e < 2; ++e)

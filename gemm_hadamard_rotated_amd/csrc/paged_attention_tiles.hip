@@ -309,7 +309,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
 #pragma unroll
         for (int n = 0; n < NB; ++n) o[n] *= keep;
       }
-      const float shift = m == kNegInf ? 0.0f : kUp - m;
+      const float shift = m == kNegInf ? 0.0f : kUp<T> - m;
       U4 pr[2 * EB][NP];
 #pragma unroll
       for (int st = 0; st < 2 * EB; ++st) {

@@ -474,7 +474,9 @@ pq1_status pq1_kv_append(const pq1_heads* k, const pq1_heads* v, const int64_t* 
  * second product as the cache's type (for an fp32 result as two or three such
  * numbers, which hold at least 22 bits), as its matrix instructions take them,
  * and an f16 probability to no less than 2^-33 of the row's largest; products
- * and the sum of the probabilities as taken are summed in fp32.  An infinity or
+ * and the sum of the probabilities as taken are summed in fp32 (which holds
+ * 2^14 keys whose bf16 values are of any finite size, and any number of values
+ * below 2^111).  An infinity or
  * NaN in a key or value reaches the rows that see it (an infinity as itself, or
  * as NaN where its probability is below 2^-31 of the row's largest) and no
  * others. */

@@ -116,3 +116,32 @@ def test_many_small_probabilities_of_f16(pq, dev, B, rows, stated, D):
                                   + 2.0 ** -24)
     worst = float((got - o).abs().max())
     assert worst <= bound, f"off by {worst:.3e}, bound {bound:.3e}"
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("rows,kv,D", [(1, 1, 64), (1, 3000, 256), (5, 700, 128), (90, 900, 64),
+                                       (300, 300, 256)])
+def test_largest_finite_values(pq, dev, rows, kv, D, out):
+    """bf16 values up to the largest number: their average is finite."""
+    s = Batch(pq, dev, [rows], [kv], 1, 2, D, 16, BF16, seed=kv)
+    s.v[0] = (s.v[0].sign() * 1.5 * 2.0 ** 120).to(BF16)
+    s.v[0][..., ::3] = torch.finfo(BF16).max
+    s.v[0][..., 1::3] = -torch.finfo(BF16).max
+    s.fill()
+    for stated in (1, kv, 10 ** 6):
+        check_rows(s, s.run(max_kv=stated, out_dtype=out), f"stated {stated}")
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("rows", [1, 90])
+def test_small_values(pq, dev, rows, out):
+    """Values near the small end of bf16: products keep the bits of fp32 down to
+    2^-149, which is 2^-129 of a probability of one (one such loss a product)."""
+    s = Batch(pq, dev, [rows], [400], 1, 2, 64, 16, BF16, seed=2)
+    s.v[0] = (s.v[0].double() * 2.0 ** -110).to(BF16)
+    s.fill()
+    for stated in (1, 10 ** 6):
+        got = s.run(max_kv=stated, out_dtype=out)
+        e, w, spread = attention_rows(s.q, s.k[0], s.v[0], s.D ** -0.5)
+        b = ref.attention_bound(e, w, spread, 400, 0.0, 64, BF16, out) + 3 * 400 * 2.0 ** -129
+        check(got, e, b, f"stated {stated}")
