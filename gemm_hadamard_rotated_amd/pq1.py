@@ -674,9 +674,11 @@ _PAIRINGS = {"halves": PQ1_ROPE_HALVES, "adjacent": PQ1_ROPE_ADJACENT}
 # integers, the stream comes from torch's raw accessor (0.1 us; a Stream object
 # takes 2), and what a Rope or a KVCache can check is checked when it is made.
 # A result is made like its input, in plain order (1.3 us; by its sizes 2.1).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# A torch without GPU support has no such accessors; it has no tensors either
+# that would get as far as their use.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _plain = torch.contiguous_format
-_current_device = torch._C._cuda_getDevice
 
 
 def _refuse(t, name: str, dtypes, dev, shape=None):
