@@ -697,6 +697,8 @@ def _refuse(t, name: str, dtypes, dev, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D, [tokens][heads][dim]")
+    if t.shape[1] >> 31 or t.shape[2] >> 31:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: heads and dim are 32-bit numbers")
     raise ValueError(f"{name}: the elements of a head must be contiguous")
 
 
@@ -707,7 +709,7 @@ def _need_heads(t: torch.Tensor, name: str, dtypes, dev=None):
         dt, size = t.dtype, t.shape
         ts, hs, ds = t.stride()
         if dt not in dtypes or (not t.is_cuda if dev is None else t.device != dev) or (
-                ds != 1 and size[2] != 1):
+                ds != 1 and size[2] != 1) or size[1] >> 31 or size[2] >> 31:
             _refuse(t, name, dtypes, dev)
     except (AttributeError, ValueError):  # no tensor, or not of three axes
         _refuse(t, name, dtypes, dev)
@@ -760,8 +762,8 @@ class Rope:
                  freqs: torch.Tensor, pairing: str = "halves", interleaved: bool = False):
         _need(freqs, "freqs", (torch.float64,))
         rot = int(rot)
-        if rot < 2 or rot % 2 != 0:
-            raise Pq1Error(2, "Rope", f"rot must be even and at least 2, got {rot}")
+        if rot < 2 or rot % 2 != 0 or rot >> 31:
+            raise Pq1Error(2, "Rope", f"rot must be even, at least 2 and below 2^31, got {rot}")
         _need_numel(freqs, "freqs", rot // 2)
         sections = [rot // 2] if sections is None else [int(s) for s in sections]
         if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != rot // 2:
@@ -824,6 +826,9 @@ class KVCache:
         if k.dim() != 4:
             raise ValueError("k must be 4-D, [pages][heads][page_size][dim]")
         _same(v.shape, k.shape, "v")
+        if max(k.shape[1:]) >> 31:
+            raise ValueError(f"k has shape {tuple(k.shape)}: heads, page_size and dim are 32-bit "
+                             f"numbers")
         self.k, self.v = k, v
         self.pages, self.heads, self.page_size, self.dim = (int(n) for n in k.shape)
         self.dtype, self.device = k.dtype, k.device
@@ -904,6 +909,17 @@ def _grow_attention_workspace(key, need: int, device: torch.device):
         return old
 
 
+def _hints_and_window(max_q: int, max_kv: int, window: int):
+    """The three as numbers of the C call's widths (64, 64 and 32 bits), which
+    would take any others by their low bits: past all lengths, or below zero,
+    every number says the same."""
+    max_q, max_kv, window = int(max_q), int(max_kv), int(window)
+    if max_q >> 62 or max_kv >> 62 or window >> 31:
+        hint = lambda n: max(-1, min(n, 1 << 62))
+        return hint(max_q), hint(max_kv), max(-1, min(window, 0x7fffffff))
+    return max_q, max_kv, window
+
+
 def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
                         cu_q: torch.Tensor, kv_len: torch.Tensor, max_q: int, max_kv: int,
                         scale: Optional[float] = None, causal: bool = True, window: int = 0,
@@ -944,8 +960,9 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
         ov, out_size = _need_heads(out, "out", (dt, torch.float32), dev)
         _same(out_size, size, "out")
     lib = _lib or load_library()
-    args = (qv, ov, cache._struct, table, max_pages, cu, lens, B, T, Hq, int(max_q), int(max_kv),
-            D ** -0.5 if scale is None else float(scale), 1 if causal else 0, int(window))
+    max_q, max_kv, window = _hints_and_window(max_q, max_kv, window)
+    args = (qv, ov, cache._struct, table, max_pages, cu, lens, B, T, Hq, max_q, max_kv,
+            D ** -0.5 if scale is None else float(scale), 1 if causal else 0, window)
     if _current_device() == dev.index:
         _attend(lib, dev, cache.heads, args)
     else:

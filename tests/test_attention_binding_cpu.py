@@ -29,3 +29,16 @@ except ValueError as e:
     p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, stdout=subprocess.PIPE,
                        stderr=subprocess.STDOUT, text=True)
     assert p.returncode == 0 and "raised" in p.stdout, p.stdout
+
+
+def test_hints_and_window_of_any_size():
+    f = pq1._hints_and_window
+    assert f(1, 700, 0) == (1, 700, 0) and f(0, 0, 2 ** 31 - 1) == (0, 0, 2 ** 31 - 1)
+    assert f(-1, -1, -1) == (-1, -1, -1)
+    for n in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 64 + 5):
+        assert f(1, 1, n) == (1, 1, 2 ** 31 - 1)
+    for n in (2 ** 62, 2 ** 63, 2 ** 64 + 5):
+        assert f(n, 3, 0) == (2 ** 62, 3, 0) and f(3, n, 0) == (3, 2 ** 62, 0)
+    for n in (-2 ** 31 - 1, -2 ** 32 + 5, -2 ** 64 + 5):
+        q, kv, w = f(n, n, n)
+        assert q < 0 and kv < 0 and w == -1

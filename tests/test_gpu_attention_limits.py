@@ -145,3 +145,22 @@ def test_small_values(pq, dev, rows, out):
         e, w, spread = attention_rows(s.q, s.k[0], s.v[0], s.D ** -0.5)
         b = ref.attention_bound(e, w, spread, 400, 0.0, 64, BF16, out) + 3 * 400 * 2.0 ** -129
         check(got, e, b, f"stated {stated}")
+
+
+def test_numbers_past_their_c_types(pq, dev):
+    """A window, or a number of heads, is not taken by its low 32 bits."""
+    s = Batch(pq, dev, [3], [90], 2, 2, 64, 16, BF16)
+    want = s.run()
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5):
+        assert torch.equal(s.run(window=window), want), window
+    with pytest.raises(pq.Pq1Error):
+        s.run(window=5 - 2 ** 32)
+    assert torch.equal(s.run(max_q=2 ** 64 + 1, max_kv=2 ** 63), s.run(max_q=2 ** 62, max_kv=2 ** 62))
+    rope = pq.Rope(8, freqs=pq.rope_frequencies(8, device=dev))
+    pos = torch.zeros(1, dtype=torch.int32, device=dev)
+    one = torch.zeros(1, 1, 8, dtype=BF16, device=dev)
+    with pytest.raises(ValueError, match="32-bit"):
+        pq.pq1_rope(one.expand(1, 2 ** 32 + 1, 8), pos, rope)
+    with pytest.raises(ValueError, match="32-bit"):
+        pq.pq1_kv_append(s.cache, s.cache.k[0, :, :1].transpose(0, 1), s.cache.v[0, :, :1].transpose(
+            0, 1), pos.long(), q=one[..., :1].expand(1, 2 ** 32 + 1, 64))
