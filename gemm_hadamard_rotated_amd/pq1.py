@@ -678,6 +678,7 @@ _PAIRINGS = {"halves": PQ1_ROPE_HALVES, "adjacent": PQ1_ROPE_ADJACENT}
 # that would get as far as their use.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 _plain = torch.contiguous_format
 
 
@@ -892,7 +893,9 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
 
 # Attention workspaces, one per (device, stream) and grown on demand: (tensor,
 # address, bytes).  Kept apart from the GEMV's, whose counter region must stay
-# as its calls leave it.
+# as its calls leave it.  A call captured into a graph takes its own from the
+# graph's memory instead: graphs captured on one stream may be replayed on
+# several, and beside calls that are not captured.
 _attn_ws = {}
 _NO_WS = (None, None, 0)
 
@@ -931,7 +934,8 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
     page_table [B][max_pages], cu_q [B+1] and kv_len [B] are int32 on the GPU;
     max_q and max_kv are the longest chunk and kv_len, known on the host.
     scale defaults to dim^-0.5.  out (of q's type, or fp32) is new unless
-    given; rows that no sequence owns keep what they held."""
+    given; rows that no sequence owns keep what they held.  The workspace is the
+    binding's: one for each stream, and one in each graph's own memory."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     dev, dt = cache.device, cache.dtype
@@ -975,16 +979,27 @@ def _attend(lib, dev, heads: int, args) -> None:
     """The call with the stream's present workspace; only if the library
     refuses that is the size asked for (0.5 us a call)."""
     stream = _raw_stream(dev.index)
+    if stream and _capturing():  # (the default stream cannot be captured)
+        need = _attention_workspace_bytes(lib, heads, args)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        code = lib.pq1_paged_attention(*args, ws.data_ptr() if need else None, need, stream)
+        if code != PQ1_OK:
+            _check(code, "pq1_paged_attention")
+        return
     key = (dev.index, stream)
     ws = _attn_ws.get(key, _NO_WS)
     code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
     if code == PQ1_OK:
         return
     if code in (1, 8):  # PQ1_ERR_NULL, PQ1_ERR_ARG: perhaps no workspace yet, or too small a one
-        B, T, Hq, max_q, max_kv = args[7:12]
-        need = lib.pq1_paged_attention_workspace_bytes(B, T, Hq, heads, args[2].dim, max_q, max_kv)
+        need = _attention_workspace_bytes(lib, heads, args)
         if need > ws[2]:
             ws = _grow_attention_workspace(key, need, dev)
             code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
     if code != PQ1_OK:
         _check(code, "pq1_paged_attention")
+
+
+def _attention_workspace_bytes(lib, heads: int, args) -> int:
+    B, T, Hq, max_q, max_kv = args[7:12]
+    return lib.pq1_paged_attention_workspace_bytes(B, T, Hq, heads, args[2].dim, max_q, max_kv)

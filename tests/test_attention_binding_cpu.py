@@ -3,6 +3,9 @@ on, keeps and refuses, with the library replaced by a recorder."""
 import os
 import subprocess
 import sys
+import threading
+import time
+import types
 
 import pytest
 import torch
@@ -42,3 +45,65 @@ def test_hints_and_window_of_any_size():
     for n in (-2 ** 31 - 1, -2 ** 32 + 5, -2 ** 64 + 5):
         q, kv, w = f(n, n, n)
         assert q < 0 and kv < 0 and w == -1
+
+
+class Recorder:
+    """Stands for the library: a call needs `need` bytes, takes a while, and
+    notes the workspaces it was given and the calls that overlapped."""
+
+    def __init__(self, need):
+        self.need, self.seen, self.inside, self.most = need, [], 0, 0
+
+    def pq1_paged_attention_workspace_bytes(self, *sizes):
+        return self.need
+
+    def pq1_paged_attention(self, *args):
+        address, size, stream = args[-3:]
+        if self.need and not address:
+            return 1
+        if size < self.need:
+            return 8
+        self.inside += 1
+        self.most = max(self.most, self.inside)
+        time.sleep(0.002)
+        self.inside -= 1
+        self.seen.append((address, size, stream))
+        return 0
+
+
+@pytest.fixture
+def binding(monkeypatch):
+    monkeypatch.setattr(pq1, "_raw_stream", lambda index: 77)
+    monkeypatch.setattr(pq1, "_capturing", lambda: False)
+    monkeypatch.setattr(pq1, "_attn_ws", {})
+    args = (None, None, types.SimpleNamespace(dim=64), None, 1, None, None, 1, 1, 2, 1, 9, 1.0, 1, 0)
+    return lambda lib: pq1._attend(lib, torch.device("cpu"), 2, args)
+
+
+def test_workspace_of_a_stream_is_kept_and_grown(binding):
+    lib = Recorder(2 << 20)
+    binding(lib)
+    binding(lib)
+    assert lib.seen[0] == lib.seen[1] and lib.seen[0][1] == 2 << 20
+    lib.need = 3 << 20
+    binding(lib)
+    assert lib.seen[2][1] == 3 << 20 and len(pq1._attn_ws) == 1
+
+
+def test_captured_calls_take_no_workspace_of_a_stream(binding, monkeypatch):
+    """Two captured calls, and eager ones of the same stream, share nothing that
+    outlives the capture."""
+    lib = Recorder(2 << 20)
+    binding(lib)
+    held = dict(pq1._attn_ws)
+    monkeypatch.setattr(pq1, "_capturing", lambda: True)
+    made = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(empty(*a, **k)) or made[-1])
+    binding(lib)
+    binding(lib)
+    assert pq1._attn_ws == held
+    assert len({a for a, _, _ in lib.seen}) == 3 and len(made) == 2
+    lib.need = 0
+    binding(lib)
+    assert lib.seen[-1][:2] == (None, 0) and pq1._attn_ws == held

@@ -164,3 +164,32 @@ def test_numbers_past_their_c_types(pq, dev):
     with pytest.raises(ValueError, match="32-bit"):
         pq.pq1_kv_append(s.cache, s.cache.k[0, :, :1].transpose(0, 1), s.cache.v[0, :, :1].transpose(
             0, 1), pos.long(), q=one[..., :1].expand(1, 2 ** 32 + 1, 64))
+
+
+def test_graphs_of_one_capture_stream_replayed_on_two(pq, dev):
+    """Each graph has its own partial sums: replayed at the same time on two
+    streams, with calls of its own on a third, every result is the eager one."""
+    batches = [Batch(pq, dev, [1], [60000 + 100 * i], 4, 6, 256, 64, BF16, seed=i) for i in range(3)]
+    args = [b.args() for b in batches]
+    call = lambda i, **k: pq.pq1_paged_attention(*args[i], max_q=1, max_kv=60000 + 100 * i, **k)
+    want = [call(i).clone() for i in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(i))
+        graphs.append(g)
+    for turn in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay()
+            third = call(2)
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], want[i]), f"graph {i}, turn {turn}"
+        assert torch.equal(third, want[2])
