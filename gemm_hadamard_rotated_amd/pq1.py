@@ -896,7 +896,10 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
 # as its calls leave it.  A call captured into a graph takes its own from the
 # graph's memory instead: graphs captured on one stream may be replayed on
 # several, and beside calls that are not captured.
+# A call may be two launches, parts and their join: _attn_lock keeps those of
+# two threads on one stream from coming between one another.
 _attn_ws = {}
+_attn_lock = threading.Lock()
 _NO_WS = (None, None, 0)
 
 
@@ -987,15 +990,16 @@ def _attend(lib, dev, heads: int, args) -> None:
             _check(code, "pq1_paged_attention")
         return
     key = (dev.index, stream)
-    ws = _attn_ws.get(key, _NO_WS)
-    code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
-    if code == PQ1_OK:
-        return
-    if code in (1, 8):  # PQ1_ERR_NULL, PQ1_ERR_ARG: perhaps no workspace yet, or too small a one
-        need = _attention_workspace_bytes(lib, heads, args)
-        if need > ws[2]:
-            ws = _grow_attention_workspace(key, need, dev)
-            code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
+    with _attn_lock:
+        ws = _attn_ws.get(key, _NO_WS)
+        code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
+        if code == PQ1_OK:
+            return
+        if code in (1, 8):  # PQ1_ERR_NULL, PQ1_ERR_ARG: perhaps no workspace yet, or too small a one
+            need = _attention_workspace_bytes(lib, heads, args)
+            if need > ws[2]:
+                ws = _grow_attention_workspace(key, need, dev)
+                code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
     if code != PQ1_OK:
         _check(code, "pq1_paged_attention")
 

@@ -107,3 +107,16 @@ def test_captured_calls_take_no_workspace_of_a_stream(binding, monkeypatch):
     lib.need = 0
     binding(lib)
     assert lib.seen[-1][:2] == (None, 0) and pq1._attn_ws == held
+
+
+def test_calls_of_two_threads_on_one_stream_follow_one_another(binding):
+    """The library enqueues parts and their join in one call, on one workspace:
+    no other thread's call on it may come between."""
+    lib = Recorder(2 << 20)
+    threads = [threading.Thread(target=lambda: [binding(lib) for _ in range(10)]) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(lib.seen) == 40 and lib.most == 1
+    assert len({a for a, _, _ in lib.seen}) == 1
