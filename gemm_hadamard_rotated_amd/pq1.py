@@ -772,13 +772,20 @@ class Rope:
                                       f"got {sections}")
         if pairing not in _PAIRINGS:
             raise Pq1Error(8, "Rope", f"unknown pairing {pairing!r} (halves or adjacent)")
-        self.rot, self.sections, self.axes, self.freqs = rot, sections, len(sections), freqs
+        self.rot, self.sections, self.axes = rot, sections, len(sections)
+        self._freqs_tensor = freqs
         padded = (sections + [0, 0, 0])[:4]
         self._spec = tuple(
             Pq1RopeSpec(rot, len(sections), (ctypes.c_int32 * 4)(*padded), int(bool(interleaved)),
                         _PAIRINGS[pairing], inverse) for inverse in (0, 1))
 
         self._device, self._freqs = freqs.device, freqs.data_ptr()
+
+    @property
+    def freqs(self) -> torch.Tensor:
+        """The tensor given; its address went into the rotation, so another one
+        needs another Rope."""
+        return self._freqs_tensor
 
     def _need_positions(self, positions: torch.Tensor, T: int, dev) -> int:
         if self._device != dev:
@@ -830,12 +837,22 @@ class KVCache:
         if max(k.shape[1:]) >> 31:
             raise ValueError(f"k has shape {tuple(k.shape)}: heads, page_size and dim are 32-bit "
                              f"numbers")
-        self.k, self.v = k, v
+        self._k, self._v = k, v
         self.pages, self.heads, self.page_size, self.dim = (int(n) for n in k.shape)
         self.dtype, self.device = k.dtype, k.device
         self._inputs = (torch.float32, k.dtype)
         self._struct = Pq1KvCache(k.data_ptr(), v.data_ptr(), _TYPE_CODE[k.dtype],
                                   self.page_size, self.pages, self.heads, self.dim)
+
+    # The tensors given; their addresses went into the struct, so other ones
+    # need another KVCache.
+    @property
+    def k(self) -> torch.Tensor:
+        return self._k
+
+    @property
+    def v(self) -> torch.Tensor:
+        return self._v
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, dim: int,

@@ -120,3 +120,11 @@ def test_calls_of_two_threads_on_one_stream_follow_one_another(binding):
         t.join()
     assert len(lib.seen) == 40 and lib.most == 1
     assert len({a for a, _, _ in lib.seen}) == 1
+
+
+@pytest.mark.parametrize("cls,name", [(pq1.KVCache, "k"), (pq1.KVCache, "v"), (pq1.Rope, "freqs")])
+def test_tensors_whose_address_is_kept_cannot_be_exchanged(cls, name):
+    """The calls would go on with the old tensor's memory."""
+    held = object.__new__(cls)
+    with pytest.raises(AttributeError):
+        setattr(held, name, torch.zeros(4))
