@@ -30,6 +30,7 @@ struct Dims {
   FastDiv parts;       // workgroups that share a token group
   FastDiv pairs;       // rot / 2 (1 without rotation)
   int tokens;          // tokens of a group
+  int64_t first;       // group of this launch's first workgroup
   int rot_units;       // units of a head that hold pairs; the rest are copies
   int tail;            // elements of a tail's unit
 };
@@ -65,7 +66,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Dims dm) {
   __shared__ float2 table[kTable];
   const uint32_t group = dm.parts.div(blockIdx.x);
   const uint32_t part = blockIdx.x - group * dm.parts.d;
-  const int64_t t0 = static_cast<int64_t>(group) * dm.tokens;
+  const int64_t t0 = (dm.first + group) * dm.tokens;
   const int nt = static_cast<int>(a.T - t0 < dm.tokens ? a.T - t0 : dm.tokens);
   const int half = a.rot >> 1;
   const uint32_t total = static_cast<uint32_t>(nt) * dm.per_token.d;
@@ -217,10 +218,15 @@ hipError_t launch_units(const RopeArgs& a, Dims dm, hipStream_t s) {
   const int64_t parts = (tokens * per_token + U * kThreads - 1) / (U * kThreads);
   dm.parts = FastDiv(static_cast<uint32_t>(parts));
   const int64_t groups = (a.T + tokens - 1) / tokens;
-  if (groups * parts >= (int64_t{1} << 32) / kThreads) return hipErrorInvalidConfiguration;
-  rope_kernel<TI, TO, VEC, U, APPEND>
-      <<<dim3(static_cast<uint32_t>(groups * parts)), kThreads, 0, s>>>(a, dm);
-  return hipGetLastError();
+  // a launch holds less than 2^32 threads
+  const int64_t most = ((int64_t{1} << 32) / kThreads - 1) / parts;
+  for (dm.first = 0; dm.first < groups; dm.first += most) {
+    const int64_t n = groups - dm.first < most ? groups - dm.first : most;
+    rope_kernel<TI, TO, VEC, U, APPEND>
+        <<<dim3(static_cast<uint32_t>(n * parts)), kThreads, 0, s>>>(a, dm);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename TI, typename TO, int VEC, bool APPEND>

@@ -193,3 +193,19 @@ def test_graphs_of_one_capture_stream_replayed_on_two(pq, dev):
         for i in range(2):
             assert torch.equal(outs[i], want[i]), f"graph {i}, turn {turn}"
         assert torch.equal(third, want[2])
+
+
+def test_rotation_past_one_launch(pq, dev):
+    """2^34 elements in pieces of two are more workgroups than a launch holds."""
+    H, D, T = 1024, 8, 2 ** 21 + 5
+    x = torch.randn(1, H, D, generator=torch.Generator().manual_seed(1)).to(BF16).to(dev)
+    pos = torch.arange(T, dtype=torch.int32, device=dev)
+    rope = pq.Rope(2, freqs=torch.tensor([0.37], dtype=torch.float64, device=dev))
+    y = torch.full((T, H, D), 7.0, dtype=BF16, device=dev)
+    pq.pq1_rope(x.expand(T, H, D), pos, rope, out=y)
+    some = torch.tensor([0, 1, 2 ** 20, 2 ** 21 - 2, 2 ** 21 - 1, 2 ** 21, T - 2, T - 1], device=dev)
+    want = pq.pq1_rope(x.expand(8, H, D), pos[some].contiguous(), rope)
+    assert torch.equal(y[some], want)
+    assert not bool((y[:, :, 2:] == 7.0).all(-1).all(-1).any())      # no token left out
+    del y
+    torch.cuda.empty_cache()
