@@ -145,15 +145,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
     const int k0 = pt.start + split * pt.chunk;
     const int k1 = pt.hi - k0 < pt.chunk ? pt.hi : k0 + pt.chunk;
 
-    // this wave's rows, and the keys that some of them sees
-    const int wr0 = static_cast<int>(r0) + 32 * wave;
-    int wlo = 0, whi = 0;
-    if (wr0 < rows) {
-      int t;
-      const int last = (wr0 + 32 < rows ? wr0 + 32 : rows) - 1;
-      visible(a, s, a.by_G.div(wr0), &wlo, &t);
-      visible(a, s, a.by_G.div(last), &t, &whi);
-    }
+    const int wr0 = static_cast<int>(r0) + 32 * wave;  // this wave's rows
     U4 q[D / 16];
     {
       const int r = wr0 + col;
