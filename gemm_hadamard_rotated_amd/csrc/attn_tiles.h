@@ -128,6 +128,27 @@ template <typename T>
 constexpr float kUp = __is_same(T, bf16) ? -20.0f : 8.0f;
 constexpr float kLag = 6.0f;
 
+// Scores (times scale_log2) past 2^24 are further apart than 1 from one float to
+// the next, so a maximum that is rounded to one may be far from itself: its
+// probability would be out of a two-byte number's range.  There the maximum is
+// rounded down, and a score's distance from it, which one fused operation gives
+// exactly, is held to the lag; that is within the rounding of such scores.
+__device__ __forceinline__ bool is_far(float m) {
+  const float a = __builtin_fabsf(m);
+  return a >= 0x1p24f && a < __builtin_inff();
+}
+// raw * scale_log2, rounded down where it is far
+__device__ __forceinline__ float scaled_max(float raw, float scale_log2) {
+  const float top = raw * scale_log2;
+  if (!is_far(top) || fmaf(raw, scale_log2, -top) >= 0.0f) return top;
+  return __int_as_float(__float_as_int(top) + (top > 0.0f ? -1 : 1));
+}
+// a score whose distance from zero is that of sc from m
+__device__ __forceinline__ float near_score(float sc, float scale_log2, float m) {
+  const float d = fmaf(sc, scale_log2, -m);
+  return (d > kLag ? kLag : d) * __builtin_amdgcn_rcpf(scale_log2);
+}
+
 // A probability as NP two-byte numbers whose sum it is: one where the result
 // is rounded to that type anyway; for an fp32 result three bf16 or two f16,
 // which hold all 24 or 22 bits.  An infinite value times each of them has to

@@ -267,16 +267,26 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void few_rows_kernel
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[rb][e][i]);
-        top = max_groups(top) * a.scale_log2;
-        if (__any(top > m[rb] + kLag)) {
-          const float up = fmaxf(m[rb], top);
+        top = max_groups(top);
+        if (__any(top * a.scale_log2 > m[rb] + kLag)) {
+          const float up = fmaxf(m[rb], scaled_max(top, a.scale_log2));
           const float keep = m[rb] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[rb] - up);
           m[rb] = up;
           l[rb] *= keep;
 #pragma unroll
           for (int n = 0; n < NO; ++n) o[rb][n] *= keep;
         }
-        const float shift = m[rb] == kNegInf ? 0.0f : kUp<T> - m[rb];
+        float shift = m[rb] == kNegInf ? 0.0f : kUp<T> - m[rb];
+        if (__any(is_far(m[rb]))) {
+          const bool far = is_far(m[rb]);
+          shift = far ? kUp<T> : shift;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sc[rb][e][i] =
+                  far ? near_score(sc[rb][e][i], a.scale_log2, m[rb]) : sc[rb][e][i];
+        }
         float p[8];
 #pragma unroll
         for (int e = 0; e < 2; ++e)

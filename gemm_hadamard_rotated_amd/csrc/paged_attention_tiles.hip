@@ -292,16 +292,25 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
         for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[e][i]);
       const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top),
                                                        false, false);
-      top = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])) * a.scale_log2;
-      if (__any(top > m + kLag)) {
-        const float up = fmaxf(m, top);
+      top = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+      if (__any(top * a.scale_log2 > m + kLag)) {
+        const float up = fmaxf(m, scaled_max(top, a.scale_log2));
         const float keep = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - up);
         m = up;
         l *= keep;
 #pragma unroll
         for (int n = 0; n < NB; ++n) o[n] *= keep;
       }
-      const float shift = m == kNegInf ? 0.0f : kUp<T> - m;
+      float shift = m == kNegInf ? 0.0f : kUp<T> - m;
+      if (__any(is_far(m))) {
+        const bool far = is_far(m);
+        shift = far ? kUp<T> : shift;
+#pragma unroll
+        for (int e = 0; e < EB; ++e)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            sc[e][i] = far ? near_score(sc[e][i], a.scale_log2, m) : sc[e][i];
+      }
       U4 pr[2 * EB][NP];
 #pragma unroll
       for (int st = 0; st < 2 * EB; ++st) {

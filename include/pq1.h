@@ -470,16 +470,16 @@ pq1_status pq1_kv_append(const pq1_heads* k, const pq1_heads* v, const int64_t* 
  *   dim is 64, 128 or 256; Hq a multiple of the cache's heads; T * Hq is
  *   at most 0x7ff00000, the pages' row count (pages * heads * page_size) 2^40.
  * Results do not depend on scheduling: the key range is split by the call's
- * sizes alone and the parts are joined in order.  Probabilities enter the
- * second product as the cache's type (for an fp32 result as two or three such
+ * sizes alone and the parts are joined in order.  Scores are summed in fp32, and
+ * they and scale * log2(e) times them have to be within it.  Probabilities enter
+ * the second product as the cache's type (for an fp32 result as two or three such
  * numbers, which hold at least 22 bits), as its matrix instructions take them,
  * and an f16 probability to no less than 2^-33 of the row's largest; products
  * and the sum of the probabilities as taken are summed in fp32 (which holds
  * 2^14 keys whose bf16 values are of any finite size, and any number of values
- * below 2^111).  An infinity or
- * NaN in a key or value reaches the rows that see it (an infinity as itself, or
- * as NaN where its probability is below 2^-31 of the row's largest) and no
- * others. */
+ * below 2^111).  An infinity or NaN in a key or value reaches the rows that see
+ * it (an infinity as itself, or as NaN where its probability is below 2^-31 of
+ * the row's largest) and no others. */
 pq1_status pq1_paged_attention(const pq1_heads* q, const pq1_heads* out,
                                const pq1_kv_cache* cache, const int32_t* page_table,
                                int64_t max_pages, const int32_t* cu_q, const int32_t* kv_len,

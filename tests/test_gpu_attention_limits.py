@@ -209,3 +209,36 @@ def test_rotation_past_one_launch(pq, dev):
     assert not bool((y[:, :, 2:] == 7.0).all(-1).all(-1).any())      # no token left out
     del y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt,size,scale", [(F16, 2.0 ** 14.3, 0.7), (F16, 2.0 ** 14.3, 50.0),
+                                           (BF16, 2.0 ** 21.7, 0.1), (BF16, 2.0 ** 40.2, 3.0)])
+@pytest.mark.parametrize("rows,D", [(1, 256), (5, 64), (90, 128), (40, 256), (300, 64)])
+def test_scores_past_the_steps_of_fp32(pq, dev, dt, size, scale, rows, D):
+    """Scores of which neighbouring floats are further apart than 1: the largest
+    takes all, equal ones share, whatever the sign.  (Scores here differ by 2^-6
+    of themselves, far more than their rounding, 2^-24 of themselves.)"""
+    kv = 700
+    s = Batch(pq, dev, [rows], [kv], 1, 2, D, 16, dt, seed=D)
+    g = torch.Generator().manual_seed(rows)
+    for sign in (1.0, -1.0):
+        s.q = torch.zeros(rows, 2, D, dtype=dt)
+        s.q[:, 0, 0], s.q[:, 1, 0] = size, size / 2
+        level = torch.randint(1, 60, (kv,), generator=g)       # larger level, larger score
+        s.k[0] = torch.zeros(kv, 1, D, dtype=dt)
+        step = level if sign > 0 else 61 - level
+        s.k[0][:, 0, 0] = sign * size * (0.03 * step.double()).to(dt)
+        s.fill()
+        k0 = sign * s.k[0][:, 0, 0].double()
+        order = k0 if sign > 0 else -k0
+        o = torch.zeros(rows, 2, D, dtype=torch.float64)
+        for i in range(rows):
+            sees = order[:kv - rows + i + 1]
+            top = sees == sees.max()
+            o[i] = s.v[0][:kv - rows + i + 1, 0][top].double().mean(0)
+        for out in (dt, F32):
+            for stated in (1, kv, 10 ** 6):
+                got = s.run(max_kv=stated, scale=scale, out_dtype=out)
+                # equal probabilities: sums in 32 bits, a rounding to the type
+                b = o.abs() * 0 + kv * 2.0 ** -23 * 5
+                check(got, o, ref.rounded_bound(o, b, out), f"sign {sign}, stated {stated}")
