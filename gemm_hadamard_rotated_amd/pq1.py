@@ -801,7 +801,8 @@ def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
     """x [T][H][D] rotated by positions ([axes][T] int32, or [T] for one axis).
 
     x may be a slice (contiguous heads); out may be x itself.  inverse=True
-    turns back, which is also the gradient of the forward call."""
+    turns back, which is also the gradient of the forward call (like all calls
+    here it is not recorded by autograd: results do not require a gradient)."""
     xv, size = _need_heads(x, "x", _FLOATS)
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")

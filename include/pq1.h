@@ -415,8 +415,9 @@ typedef struct {
  *   positions  [axes][T] int32, of any sign (4-byte aligned).
  *   freqs      [rot / 2] fp64, radians per position (8-byte aligned).
  *   T >= 0 (0 does nothing), H >= 1, D a multiple of 8 up to 1024.
- * Angles are reduced in fp64: a position of any size loses nothing beyond the
- * fp32 rounding of the reduced angle. */
+ * An angle is taken and reduced in fp64, where it is off by less than 2^-51 of
+ * itself, and narrowed to fp32 then: below 2^25 radians that rounding is what
+ * counts. */
 pq1_status pq1_rope(const pq1_heads* x, const pq1_heads* y, const int32_t* positions,
                     const double* freqs, const pq1_rope_spec* spec, int64_t T, int32_t H,
                     int32_t D, void* stream);
