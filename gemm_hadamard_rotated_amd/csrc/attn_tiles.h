@@ -175,6 +175,10 @@ __device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) 
     for (int t = 0; t < 8; ++t) v[t] = static_cast<T>(p[t]);
     out[0] = __builtin_bit_cast(U4, v);
   } else if constexpr (__is_same(T, f16)) {
+    // p - c, exact, in one operation of mixed types (which the compiler does not
+    // make of a difference: 8192 rows of 8 heads, 7168 keys, D = 64 254 -> 241 us)
+    float minus = -1.0f;
+    asm("" : "+s"(minus));
     Vec8<f16> rest;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -185,7 +189,7 @@ __device__ __forceinline__ void split_probs(const float (&p)[8], U4 (&out)[NP]) 
       out[0][w] = __builtin_bit_cast(uint32_t, c);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        rest[2 * w + t] = static_cast<f16>(p[2 * w + t] - static_cast<float>(c[t]));
+        rest[2 * w + t] = static_cast<f16>(fmaf(static_cast<float>(c[t]), minus, p[2 * w + t]));
     }
     out[1] = __builtin_bit_cast(U4, rest);
   } else {
