@@ -698,8 +698,6 @@ def _refuse(t, name: str, dtypes, dev, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D, [tokens][heads][dim]")
-    if t.shape[1] >> 31 or t.shape[2] >> 31:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}: heads and dim are 32-bit numbers")
     raise ValueError(f"{name}: the elements of a head must be contiguous")
 
 
@@ -710,7 +708,7 @@ def _need_heads(t: torch.Tensor, name: str, dtypes, dev=None):
         dt, size = t.dtype, t.shape
         ts, hs, ds = t.stride()
         if dt not in dtypes or (not t.is_cuda if dev is None else t.device != dev) or (
-                ds != 1 and size[2] != 1) or size[1] >> 31 or size[2] >> 31:
+                ds != 1 and size[2] != 1):
             _refuse(t, name, dtypes, dev)
     except (AttributeError, ValueError):  # no tensor, or not of three axes
         _refuse(t, name, dtypes, dev)
@@ -725,6 +723,10 @@ def _need_vector(t: torch.Tensor, name: str, dtype: torch.dtype, dev, shape) -> 
             or t.shape != shape or not t.is_contiguous():
         _refuse(t, name, (dtype,), dev, shape)
     return t.data_ptr()
+
+
+def _too_many(size, name: str):
+    raise ValueError(f"{name} has shape {tuple(size)}: heads and dim are 32-bit numbers")
 
 
 def _same(size, expected, name: str):
@@ -808,6 +810,8 @@ def pq1_rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope,
         raise TypeError("rope must be a Rope")
     dev = x.device
     T, H, D = size
+    if H >> 31 or D >> 31:
+        _too_many(size, "x")
     pos = rope._need_positions(positions, T, dev)
     if out is None:
         dt = x.dtype if out_dtype is None else out_dtype
@@ -896,6 +900,8 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
         qv, size = _need_heads(q, "q", kind, dev)
         Hq = size[1]
         _same(size, (T, Hq, cache.dim), "q")
+        if Hq >> 31:
+            _too_many(size, "q")
         if q_out is None:
             q_out = torch.empty_like(q, dtype=dt, memory_format=_plain)
             ov = Pq1Heads(q_out.data_ptr(), _TYPE_CODE[dt], Hq * cache.dim, cache.dim)
@@ -964,6 +970,8 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
     T, Hq, D = size
     if D != cache.dim:
         raise ValueError(f"q has shape {tuple(size)}, expected {(T, Hq, cache.dim)}")
+    if Hq >> 31:
+        _too_many(size, "q")
     if not isinstance(page_table, torch.Tensor):
         raise TypeError("page_table must be a torch.Tensor")
     if page_table.dim() != 2:

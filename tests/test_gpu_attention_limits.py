@@ -163,7 +163,7 @@ def test_numbers_past_their_c_types(pq, dev):
         pq.pq1_rope(one.expand(1, 2 ** 32 + 1, 8), pos, rope)
     with pytest.raises(ValueError, match="32-bit"):
         pq.pq1_kv_append(s.cache, s.cache.k[0, :, :1].transpose(0, 1), s.cache.v[0, :, :1].transpose(
-            0, 1), pos.long(), q=one[..., :1].expand(1, 2 ** 32 + 1, 64))
+            0, 1), pos.long(), q=one.repeat(1, 1, 8).expand(1, 2 ** 32 + 1, 64))
 
 
 def test_graphs_of_one_capture_stream_replayed_on_two(pq, dev):
