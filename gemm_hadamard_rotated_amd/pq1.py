@@ -943,11 +943,8 @@ def _hints_and_window(max_q: int, max_kv: int, window: int):
     """The three as numbers of the C call's widths (64, 64 and 32 bits), which
     would take any others by their low bits: past all lengths, or below zero,
     every number says the same."""
-    max_q, max_kv, window = int(max_q), int(max_kv), int(window)
-    if max_q >> 62 or max_kv >> 62 or window >> 31:
-        hint = lambda n: max(-1, min(n, 1 << 62))
-        return hint(max_q), hint(max_kv), max(-1, min(window, 0x7fffffff))
-    return max_q, max_kv, window
+    hint = lambda n: max(-1, min(n, 1 << 62))
+    return hint(max_q), hint(max_kv), max(-1, min(window, 0x7fffffff))
 
 
 def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
@@ -993,7 +990,9 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
         ov, out_size = _need_heads(out, "out", (dt, torch.float32), dev)
         _same(out_size, size, "out")
     lib = _lib or load_library()
-    max_q, max_kv, window = _hints_and_window(max_q, max_kv, window)
+    max_q, max_kv, window = int(max_q), int(max_kv), int(window)
+    if max_q >> 62 or max_kv >> 62 or window >> 31:
+        max_q, max_kv, window = _hints_and_window(max_q, max_kv, window)
     args = (qv, ov, cache._struct, table, max_pages, cu, lens, B, T, Hq, max_q, max_kv,
             D ** -0.5 if scale is None else float(scale), 1 if causal else 0, window)
     if _current_device() == dev.index:
