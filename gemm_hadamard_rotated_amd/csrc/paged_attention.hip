@@ -23,8 +23,8 @@ namespace {
 // V, and picking one dimension of the 8 keys is a byte permute of registers.
 //
 // Bound: reading the cache; a call of one token by its fixed cost.  One token
-// at 131071 keys (4 cache heads, D = 256): 99 us, 5.4 TB/s (a large copy
-// reaches 5.1, a cached one more); 64 tokens at 200 to 8000 keys: 232 us, 4.9
+// at 131071 keys (4 cache heads, D = 256): 98 us, 5.5 TB/s (a large copy
+// reaches 5.1, a read alone 6.5); 64 tokens at 200 to 8000 keys: 231 us, 4.9
 // TB/s; one token at 701 keys: 8 us for this kernel and 4.2 for the join, where
 // an empty kernel takes 3.  What paid: as many workgroups as CUs (twice as
 // many: 109 and 239 us), divisions by multiplication, lengths and page numbers

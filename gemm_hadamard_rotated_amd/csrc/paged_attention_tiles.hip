@@ -14,9 +14,12 @@
 // and a row's maximum and sum need one exchange between the halves of a wave.
 //
 // Bound: the matrix instructions and, for small D, the softmax between them.
-// 8192 rows of 8 cache heads against 7168 keys take 439 us at D = 256 (1096
-// TFLOP/s), 260 us at 128 (925) and 187 us at 64 (644); a large library product
-// reaches 1263 TFLOP/s on the same card.
+// 8192 rows of 8 cache heads against 7168 keys take 445 to 454 us at D = 256
+// (1061 to 1082 TFLOP/s), 255 to 261 us at 128 (921 to 945) and 186 to 188 us at
+// 64 (641 to 646); a large library product reaches 1263 TFLOP/s on the same card.
+// An fp32 result takes the second product three times for bf16 caches, 769 to
+// 792, 429 to 440 and 318 to 324 us, and twice for f16, 658 to 681, 362 to 376
+// and 238 to 241 us.
 // What was measured on the way (D = 128 of the above unless said): 64 rows a
 // wave, one wave a SIMD: slower (759 against 505 us for 2048 tokens after 6144
 // at D = 256); page numbers from LDS and no load waited for in the loop, so

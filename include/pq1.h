@@ -355,7 +355,8 @@ pq1_status pq1_embed(const int32_t* tokens, int64_t M, const uint32_t* w_bits, c
  * (t, h, d) is at data[t * token_stride + h * head_stride + d] (strides in
  * elements, not negative).  A slice of a stacked projection's output is such
  * an array.  data is 16-byte aligned and both strides are multiples of 16
- * bytes (PQ1_ERR_ALIGN). */
+ * bytes (PQ1_ERR_ALIGN).  Strides are at most 2^31; a call takes less than 2^30
+ * tokens, at most 1024 heads and 2^38 elements in all (PQ1_ERR_SHAPE). */
 typedef struct {
     void* data;
     int32_t dtype;
@@ -415,6 +416,7 @@ typedef struct {
  *   positions  [axes][T] int32, of any sign (4-byte aligned).
  *   freqs      [rot / 2] fp64, radians per position (8-byte aligned).
  *   T >= 0 (0 does nothing), H >= 1, D a multiple of 8 up to 1024.
+ * One launch, or several where T H D is past 2^34.
  * An angle is taken and reduced in fp64, where it is off by less than 2^-51 of
  * itself, and narrowed to fp32 then: below 2^25 radians that rounding is what
  * counts. */
@@ -423,7 +425,7 @@ pq1_status pq1_rope(const pq1_heads* x, const pq1_heads* y, const int32_t* posit
                     int32_t D, void* stream);
 
 /* Append T tokens to the cache and rotate keys (and queries) on the way, in
- * one launch: row slots[t] of every page head gets the rotated key and the
+ * one launch (or several, as above): row slots[t] of every page head gets the rotated key and the
  * value of token t.
  *   k, v       [T][cache heads][cache dim] views of one type, fp32 or the
  *              cache's.
@@ -469,7 +471,8 @@ pq1_status pq1_kv_append(const pq1_heads* k, const pq1_heads* v, const int64_t* 
  *              matter and is not kept; calls that may overlap in time need
  *              different workspaces.
  *   dim is 64, 128 or 256; Hq a multiple of the cache's heads; T * Hq is
- *   at most 0x7ff00000, the pages' row count (pages * heads * page_size) 2^40.
+ *   at most 0x7ff00000, B * heads less than 2^23, the pages' row count (pages *
+ *   heads * page_size) 2^40.
  * Results do not depend on scheduling: the key range is split by the call's
  * sizes alone and the parts are joined in order.  Scores are summed in fp32, and
  * they and scale * log2(e) times them have to be within it.  Probabilities enter
