@@ -43,7 +43,7 @@ ARCH = "gfx950"
 
 SOURCES = ["api.hip", "rotate.hip", "gemv.hip", "gemv_packed.hip", "gemm.hip", "gemm_skinny.hip",
            "api_attention.hip", "rope.hip", "paged_attention.hip",
-           "paged_attention_tiles.hip"]
+           "paged_attention_tiles.hip", "api_kv4.hip", "norm_rope.hip", "kv4_read.hip"]
 BENCH_SOURCES = ["bench_kernels.hip"]
 
 # gemm_skinny.hip: MFMA results stay in ordinary VGPRs (the per-group fold

@@ -56,6 +56,44 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, int in_dtype, int out_dtype, hipStream_t s);
 
+// One launch of the norm and rotation kernel: streams as above, each head over the
+// root of its mean square and times a weight first.
+struct NormArgs {
+  RopeArgs rope;
+  const float* x_weight = nullptr;  // null: no norm of x
+  const float* k_weight = nullptr;
+  double eps = 0;
+  uint8_t* k_scale = nullptr;  // of a 4-bit cache
+  uint8_t* v_scale = nullptr;
+  const void* grad = nullptr;  // of y, for the gradient of x, which goes to y's place
+  int64_t g_ts = 0, g_hs = 0;
+};
+hipError_t launch_norm_rope(const NormArgs& a, int in_dtype, int out_dtype, bool cache4,
+                            hipStream_t s);
+// part_dw: norm_grad_parts(T) * D floats, null without dw.
+hipError_t launch_norm_rope_grad(const NormArgs& a, int g_dtype, int x_dtype, float* dw,
+                                 float* part_dw, hipStream_t s);
+// Workgroups of the gradient kernel: what fills the device four times.
+inline int64_t norm_grad_parts(int64_t T) { return T < 1024 ? T : 1024; }
+
+// Rows of a 4-bit cache as numbers of out_dtype.
+struct Read4Args {
+  const uint8_t* k = nullptr;
+  const uint8_t* k_scale = nullptr;
+  const uint8_t* v = nullptr;
+  const uint8_t* v_scale = nullptr;
+  const int64_t* slots = nullptr;
+  int64_t slot_count = 0;
+  int page_shift = 0;
+  void* k_out = nullptr;  // null: not wanted
+  int64_t k_ts = 0, k_hs = 0;
+  void* v_out = nullptr;
+  int64_t v_ts = 0, v_hs = 0;
+  int64_t T = 0;
+  int H = 0, D = 0;
+};
+hipError_t launch_kv4_read(const Read4Args& a, int out_dtype, hipStream_t s);
+
 struct AttnArgs {
   const void* q = nullptr;
   int64_t q_ts = 0, q_hs = 0;

@@ -40,7 +40,9 @@ EXPORTS = ("pq1_rotate", "pq1_gemv_workspace_bytes", "pq1_gemv", "pq1_gemv_ex",
            "pq1_gemv_packed_ex", "pq1_rotate_gemv_packed_ex", "pq1_gemm", "pq1_gemm_ex",
            "pq1_status_str", "pq1_abi_version", "pq1_last_hip_error", "pq1_set_test_flags",
            "pq1_rotate_gemv_packed_noalloc", "pq1_rope", "pq1_kv_append",
-           "pq1_paged_attention", "pq1_paged_attention_workspace_bytes")
+           "pq1_paged_attention", "pq1_paged_attention_workspace_bytes", "pq1_norm_rope",
+           "pq1_norm_rope_grad", "pq1_norm_rope_grad_workspace_bytes", "pq1_kv_append_ex",
+           "pq1_kv4_append", "pq1_kv4_read")
 
 
 class Pq1Error(RuntimeError):
@@ -70,6 +72,18 @@ class Pq1KvCache(ctypes.Structure):
                 ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
 
 
+class Pq1HeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class Pq1Kv4Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("pages", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 
@@ -86,7 +100,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib = ctypes.CDLL(path)
         P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         PP = ctypes.POINTER(Pq1Perm)
-        PH, PS, PC = (ctypes.POINTER(c) for c in (Pq1Heads, Pq1RopeSpec, Pq1KvCache))
+        PH, PS, PC, PN, P4 = (ctypes.POINTER(c) for c in (Pq1Heads, Pq1RopeSpec, Pq1KvCache,
+                                                          Pq1HeadNorm, Pq1Kv4Cache))
+        F = ctypes.c_float
         sig = {
             "pq1_rotate": (I32, [P, P, PP, P, I32, I64, I64, P]),
             "pq1_gemv_workspace_bytes": (SZ, [I64, I64]),
@@ -113,6 +129,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "pq1_paged_attention": (I32, [PH, PH, PC, P, I64, P, P, I64, I64, I32, I64, I64,
                                           ctypes.c_float, I32, I32, P, SZ, P]),
             "pq1_paged_attention_workspace_bytes": (SZ, [I64, I64, I32, I32, I32, I64, I64]),
+            "pq1_norm_rope": (I32, [PH, PH, P, F, P, P, PS, I64, I32, I32, P]),
+            "pq1_norm_rope_grad": (I32, [PH, PH, PH, P, P, F, P, P, PS, I64, I32, I32, P, SZ, P]),
+            "pq1_norm_rope_grad_workspace_bytes": (SZ, [I64, I32]),
+            "pq1_kv_append_ex": (I32, [PH, PH, P, PH, PH, I32, P, P, PS, PN, PC, I64, P]),
+            "pq1_kv4_append": (I32, [PH, PH, P, PH, PH, I32, P, P, PS, PN, P4, I64, P]),
+            "pq1_kv4_read": (I32, [P4, P, PH, PH, I64, P]),
             "pq1_status_str": (ctypes.c_char_p, [I32]),
             "pq1_abi_version": (I32, []),
             "pq1_last_hip_error": (I32, []),
@@ -868,16 +890,53 @@ class KVCache:
                    torch.empty(shape, dtype=dtype, device=device))
 
 
-def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
-                  positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
-                  q: Optional[torch.Tensor] = None,
-                  q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
-    """Store k and v ([T][heads][dim], slices allowed, fp32 or the cache's
-    type) at slots ([T] int64, page * page_size + row; -1 is padding), keys
-    rotated by `rope`; with q, the rotated queries are returned in the cache's
-    type.  One launch."""
-    if not isinstance(cache, KVCache):
-        raise TypeError("cache must be a KVCache")
+class HeadNorm:
+    """The norms of an append's keys and queries: each head over the root of its
+    mean square (plus eps) and times a weight, [dim] fp32 on the GPU.  A weight
+    that is None leaves its heads as they are."""
+
+    def __init__(self, k_weight: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None, *,
+                 eps: float = 1e-6):
+        given = [w for w in (k_weight, q_weight) if w is not None]
+        if not given:
+            raise ValueError("a norm needs a weight")
+        for w in given:
+            _need(w, "weight", (torch.float32,), given[0].device)
+            if w.shape != given[0].shape or w.dim() != 1:
+                raise ValueError(f"weights must be 1-D, [dim], got {[tuple(w.shape) for w in given]}")
+        _need_eps(eps, "HeadNorm")
+        self._k_weight, self._q_weight, self.eps = k_weight, q_weight, float(eps)
+        self._device, self._dim = given[0].device, given[0].numel()
+        self._struct = Pq1HeadNorm(_ptr(q_weight), _ptr(k_weight), self.eps)
+
+    # The tensors given; their addresses went into the struct, so other ones
+    # need another HeadNorm.
+    @property
+    def k_weight(self) -> Optional[torch.Tensor]:
+        return self._k_weight
+
+    @property
+    def q_weight(self) -> Optional[torch.Tensor]:
+        return self._q_weight
+
+    def _need_fit(self, dim: int, dev):
+        if self._device != dev:
+            raise ValueError(f"the norm's weights are on {self._device}, expected {dev}")
+        if self._dim != dim:
+            raise ValueError(f"the norm's weights have {self._dim} elements, expected {dim}")
+        return self._struct
+
+
+def _need_eps(eps: float, where: str) -> float:
+    eps = float(eps)
+    # as the C call sees it
+    if not 2.0 ** -150 < eps < 3.4028236e38:
+        raise Pq1Error(8, where, f"eps must be above 0 and finite in fp32, got {eps}")
+    return eps
+
+
+def _append(where: str, fn, cache, k, v, slots, positions, rope, q, q_out, norm):
+    """Both appends: a launch of fn with the views of their arguments."""
     dev, dt = cache.device, cache.dtype
     kv, size = _need_heads(k, "k", cache._inputs, dev)
     T = size[0]
@@ -910,9 +969,218 @@ def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
             _same(out_size, size, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _launch(dev, "pq1_kv_append", (_lib or load_library()).pq1_kv_append, kv, vv, at, qv, ov, Hq,
-            pos, freqs, spec, cache._struct, T)
+    if fn is None:  # the 16-bit append has a call of its own without norms
+        _launch(dev, where, (_lib or load_library()).pq1_kv_append, kv, vv, at, qv, ov, Hq, pos,
+                freqs, spec, cache._struct, T)
+        return q_out
+    ns = None
+    if norm is not None:
+        if not isinstance(norm, HeadNorm):
+            raise TypeError("norm must be a HeadNorm")
+        ns = norm._need_fit(cache.dim, dev)
+    _launch(dev, where, fn, kv, vv, at, qv, ov, Hq, pos, freqs, spec, ns, cache._struct, T)
     return q_out
+
+
+def pq1_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                  positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  norm: Optional[HeadNorm] = None) -> Optional[torch.Tensor]:
+    """Store k and v ([T][heads][dim], slices allowed, fp32 or the cache's
+    type) at slots ([T] int64, page * page_size + row; -1 is padding), keys
+    rotated by `rope`; with q, the rotated queries are returned in the cache's
+    type.  `norm` (pq1_kv_append_ex) comes before the rotation.  One launch."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    fn = None if norm is None else (_lib or load_library()).pq1_kv_append_ex
+    return _append("pq1_kv_append" if norm is None else "pq1_kv_append_ex", fn, cache, k, v, slots,
+                   positions, rope, q, q_out, norm)
+
+
+class KV4Cache:
+    """A paged key/value cache of 4-bit numbers over four uint8 tensors of the
+    caller's: codes [pages][heads][page_size][dim / 2] and scales
+    [pages][heads][page_size][dim / 32] (include/pq1.h, pq1_kv4_cache).  dtype,
+    bf16 or f16, is the type of the queries and the one values are read in."""
+
+    def __init__(self, k: torch.Tensor, k_scale: torch.Tensor, v: torch.Tensor,
+                 v_scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+        _need(k, "k", (torch.uint8,))
+        for t, name in ((k_scale, "k_scale"), (v, "v"), (v_scale, "v_scale")):
+            _need(t, name, (torch.uint8,), k.device)
+        if k.dim() != 4:
+            raise ValueError("k must be 4-D, [pages][heads][page_size][dim / 2]")
+        if k.shape[3] % 16 != 0:
+            raise ValueError(f"k has shape {tuple(k.shape)}: dim must be a multiple of 32")
+        if max(k.shape[1:]) >> 30:
+            raise ValueError(f"k has shape {tuple(k.shape)}: heads, page_size and dim are 32-bit "
+                             f"numbers")
+        _same(v.shape, k.shape, "v")
+        scales = torch.Size((*k.shape[:3], k.shape[3] // 16))
+        _same(k_scale.shape, scales, "k_scale")
+        _same(v_scale.shape, scales, "v_scale")
+        self._k, self._k_scale, self._v, self._v_scale = k, k_scale, v, v_scale
+        self.pages, self.heads, self.page_size = (int(n) for n in k.shape[:3])
+        self.dim = 2 * int(k.shape[3])
+        self.dtype, self.device = dtype, k.device
+        self._inputs = (torch.float32, dtype)
+        self._struct = Pq1Kv4Cache(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
+                                   v_scale.data_ptr(), _TYPE_CODE[dtype], self.page_size,
+                                   self.pages, self.heads, self.dim)
+
+    # The tensors given; their addresses went into the struct, so other ones
+    # need another KV4Cache.
+    @property
+    def k(self) -> torch.Tensor:
+        return self._k
+
+    @property
+    def k_scale(self) -> torch.Tensor:
+        return self._k_scale
+
+    @property
+    def v(self) -> torch.Tensor:
+        return self._v
+
+    @property
+    def v_scale(self) -> torch.Tensor:
+        return self._v_scale
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, dim: int,
+              dtype: torch.dtype = torch.bfloat16, device=None) -> "KV4Cache":
+        device = torch.device("cuda") if device is None else device
+        if int(dim) % 32 != 0:
+            raise ValueError(f"dim must be a multiple of 32, got {dim}")
+        shape = (int(pages), int(heads), int(page_size))
+        make = lambda n: torch.empty((*shape, n), dtype=torch.uint8, device=device)
+        return cls(make(int(dim) // 2), make(int(dim) // 32), make(int(dim) // 2),
+                   make(int(dim) // 32), dtype)
+
+
+def pq1_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                   positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                   q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                   norm: Optional[HeadNorm] = None) -> Optional[torch.Tensor]:
+    """pq1_kv_append into a 4-bit cache: keys (after norm and rotation) and values
+    become codes and scales (include/pq1.h); queries are returned in the cache's
+    dtype.  One launch."""
+    if not isinstance(cache, KV4Cache):
+        raise TypeError("cache must be a KV4Cache")
+    return _append("pq1_kv4_append", (_lib or load_library()).pq1_kv4_append, cache, k, v, slots,
+                   positions, rope, q, q_out, norm)
+
+
+def pq1_kv4_read(cache: KV4Cache, slots: torch.Tensor, k_out: Optional[torch.Tensor] = None,
+                 v_out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None):
+    """(keys, values) of rows slots ([T] int64) of a 4-bit cache, [T][heads][dim]
+    each, in out_dtype (the cache's unless given).  Tensors may be given for both
+    or for one; then that one alone is read, and None is in the other's place.
+    Slots may repeat; one outside the cache gives zeros."""
+    if not isinstance(cache, KV4Cache):
+        raise TypeError("cache must be a KV4Cache")
+    dev = cache.device
+    T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else -1
+    at = _need_vector(slots, "slots", torch.int64, dev, (T,))
+    shape = (T, cache.heads, cache.dim)
+    if k_out is None and v_out is None:
+        dt = cache.dtype if out_dtype is None else out_dtype
+        if dt not in _TYPE_CODE:
+            raise TypeError(f"out_dtype must be in {_FLOATS}")
+        k_out = torch.empty(shape, dtype=dt, device=dev)
+        v_out = torch.empty(shape, dtype=dt, device=dev)
+        kv, vv = (Pq1Heads(t.data_ptr(), _TYPE_CODE[dt], shape[1] * shape[2], shape[2])
+                  for t in (k_out, v_out))
+    else:
+        views, kinds = [], _FLOATS if out_dtype is None else (out_dtype,)
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is None:
+                views.append(None)
+                continue
+            view, size = _need_heads(t, name, kinds, dev)
+            _same(size, shape, name)
+            views.append(view)
+            kinds = (t.dtype,)
+        kv, vv = views
+    _launch(dev, "pq1_kv4_read", (_lib or load_library()).pq1_kv4_read, cache._struct, at, kv, vv, T)
+    return k_out, v_out
+
+
+def _norm_arguments(x, weight, positions, rope, eps, where):
+    """What both norm calls check: view and shape of x, weight's address, eps, and
+    the rotation's positions, frequencies and specs (None without one)."""
+    xv, size = _need_heads(x, "x", _FLOATS)
+    dev = x.device
+    if size[1] >> 31 or size[2] >> 31:
+        _too_many(size, "x")
+    w = _need_vector(weight, "weight", torch.float32, dev, (size[2],))
+    eps = _need_eps(eps, where)
+    if rope is None:
+        return xv, size, dev, w, eps, None, None, (None, None)
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    if positions is None:
+        raise ValueError("a rotation needs positions")
+    return xv, size, dev, w, eps, rope._need_positions(positions, size[0], dev), rope._freqs, rope._spec
+
+
+def _out_like(x, size, out, out_dtype, dev, name):
+    """The result given, or one made like x: the tensor and its view."""
+    if out is None:
+        dt = x.dtype if out_dtype is None else out_dtype
+        if dt not in _TYPE_CODE:
+            raise TypeError(f"out_dtype must be in {_FLOATS}")
+        out = torch.empty_like(x, dtype=dt, memory_format=_plain)
+        return out, Pq1Heads(out.data_ptr(), _TYPE_CODE[dt], size[1] * size[2], size[2])
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"{name} has dtype {out.dtype}, out_dtype is {out_dtype}")
+    view, out_size = _need_heads(out, name, _FLOATS, dev)
+    _same(out_size, size, name)
+    return out, view
+
+
+def pq1_norm_rope(x: torch.Tensor, weight: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                  rope: Optional[Rope] = None, eps: float = 1e-6,
+                  out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                  inverse: bool = False) -> torch.Tensor:
+    """Each head of x [T][H][D] over the root of its mean square (plus eps), times
+    weight ([D] fp32), then rotated as by pq1_rope (rope None: not).  x may be a
+    slice (contiguous heads); out may be x itself.  Not recorded by autograd:
+    pq1_norm_rope_grad is the gradient."""
+    xv, size, dev, w, eps, pos, freqs, spec = _norm_arguments(x, weight, positions, rope, eps,
+                                                              "pq1_norm_rope")
+    out, yv = _out_like(x, size, out, out_dtype, dev, "out")
+    _launch(dev, "pq1_norm_rope", (_lib or load_library()).pq1_norm_rope, xv, yv, w, eps, pos, freqs,
+            spec[1 if inverse else 0], *size)
+    return out
+
+
+def pq1_norm_rope_grad(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                       positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                       eps: float = 1e-6, dx: Optional[torch.Tensor] = None,
+                       weight_grad: bool = True, inverse: bool = False):
+    """(dx, dweight) of pq1_norm_rope called with the same arguments, for a
+    gradient `grad` of its result: dx of x's type (new unless given; x or grad
+    itself may be), dweight [D] fp32, or None with weight_grad False."""
+    xv, size, dev, w, eps, pos, freqs, spec = _norm_arguments(x, weight, positions, rope, eps,
+                                                              "pq1_norm_rope_grad")
+    gv, g_size = _need_heads(grad, "grad", _FLOATS, dev)
+    _same(g_size, size, "grad")
+    dx, dv = _out_like(x, size, dx, x.dtype, dev, "dx")
+    T, H, D = size
+    lib = _lib or load_library()
+    dw = torch.empty_like(weight) if weight_grad else None
+    args = (gv, xv, dv, w, dw.data_ptr() if weight_grad else None, eps, pos, freqs,
+            spec[1 if inverse else 0], T, H, D)
+    need = lambda: lib.pq1_norm_rope_grad_workspace_bytes(T, D) if weight_grad else 0
+    if _current_device() == dev.index:
+        _with_workspace(dev, "pq1_norm_rope_grad", lib.pq1_norm_rope_grad, args, need)
+    else:
+        with torch.cuda.device(dev):
+            _with_workspace(dev, "pq1_norm_rope_grad", lib.pq1_norm_rope_grad, args, need)
+    return dx, dw
 
 
 # Attention workspaces, one per (device, stream) and grown on demand: (tensor,
@@ -1004,29 +1272,34 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
 
 
 def _attend(lib, dev, heads: int, args) -> None:
+    _with_workspace(dev, "pq1_paged_attention", lib.pq1_paged_attention, args,
+                    lambda: _attention_workspace_bytes(lib, heads, args))
+
+
+def _with_workspace(dev, where: str, fn, args, need_of) -> None:
     """The call with the stream's present workspace; only if the library
     refuses that is the size asked for (0.5 us a call)."""
     stream = _raw_stream(dev.index)
     if stream and _capturing():  # (the default stream cannot be captured)
-        need = _attention_workspace_bytes(lib, heads, args)
+        need = need_of()
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        code = lib.pq1_paged_attention(*args, ws.data_ptr() if need else None, need, stream)
+        code = fn(*args, ws.data_ptr() if need else None, need, stream)
         if code != PQ1_OK:
-            _check(code, "pq1_paged_attention")
+            _check(code, where)
         return
     key = (dev.index, stream)
     with _attn_lock:
         ws = _attn_ws.get(key, _NO_WS)
-        code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
+        code = fn(*args, ws[1], ws[2], stream)
         if code == PQ1_OK:
             return
         if code in (1, 8):  # PQ1_ERR_NULL, PQ1_ERR_ARG: perhaps no workspace yet, or too small a one
-            need = _attention_workspace_bytes(lib, heads, args)
+            need = need_of()
             if need > ws[2]:
                 ws = _grow_attention_workspace(key, need, dev)
-                code = lib.pq1_paged_attention(*args, ws[1], ws[2], stream)
+                code = fn(*args, ws[1], ws[2], stream)
     if code != PQ1_OK:
-        _check(code, "pq1_paged_attention")
+        _check(code, where)
 
 
 def _attention_workspace_bytes(lib, heads: int, args) -> int:

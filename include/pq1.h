@@ -495,6 +495,106 @@ pq1_status pq1_paged_attention(const pq1_heads* q, const pq1_heads* out,
 size_t pq1_paged_attention_workspace_bytes(int64_t B, int64_t T, int32_t Hq, int32_t heads,
                                            int32_t dim, int64_t max_q, int64_t max_kv);
 
+/* ---------------------------------------------------------------------------
+ * Norms of heads, a cache held in 4 bits, and windows whose first tokens stay
+ * visible.  Conventions as in the attention layer above.
+ * ------------------------------------------------------------------------- */
+
+/* y = rotation (as pq1_rope) of each head over the root of its mean square:
+ *   y = R(p) (w * x * r),   r = (sum_d x_d^2 / D + eps)^(-1/2).
+ *   weight   [D] fp32 (16-byte aligned).
+ *   eps      > 0 and finite (PQ1_ERR_ARG).
+ *   spec     NULL: no rotation; positions and freqs are then ignored.
+ * Everything else as pq1_rope.  The mean square is taken in fp64, so heads of
+ * any finite size have their norm; a head that holds an infinity gives NaN there
+ * and zeros elsewhere, as the formula does. */
+pq1_status pq1_norm_rope(const pq1_heads* x, const pq1_heads* y, const float* weight, float eps,
+                         const int32_t* positions, const double* freqs, const pq1_rope_spec* spec,
+                         int64_t T, int32_t H, int32_t D, void* stream);
+
+/* Gradient of pq1_norm_rope: with u = R(p)^T grad,
+ *   dweight = sum over tokens and heads of u * x * r,
+ *   dx      = r w * u - x r^3 / D sum_d (w_d u_d x_d).
+ *   grad       [T][H][D] gradient of y, of any of the three types.
+ *   x          the forward call's input; dx of its type.
+ *   dx         overlaps no input, or is grad itself or x itself (same data,
+ *              type and strides).
+ *   dweight    [D] fp32 (4-byte aligned), overwritten; or NULL.
+ *   spec       the forward call's (its `inverse` says which way that turned).
+ *   workspace  pq1_norm_rope_grad_workspace_bytes(T, D) bytes, 256-byte aligned;
+ *              may be NULL where dweight is, or where that is 0.  Its content
+ *              does not matter and is not kept; calls that may overlap in time
+ *              need different workspaces.
+ * dweight is the same from run to run: its sums are fp32 over a workgroup's heads
+ * and fp64 over workgroups, in a fixed order.  Two launches. */
+pq1_status pq1_norm_rope_grad(const pq1_heads* grad, const pq1_heads* x, const pq1_heads* dx,
+                              const float* weight, float* dweight, float eps,
+                              const int32_t* positions, const double* freqs,
+                              const pq1_rope_spec* spec, int64_t T, int32_t H, int32_t D,
+                              void* workspace, size_t workspace_bytes, void* stream);
+size_t pq1_norm_rope_grad_workspace_bytes(int64_t T, int32_t D);
+
+/* Norms of an append's queries and keys: weights [dim] fp32, 16-byte aligned.  A
+ * NULL weight leaves its heads without norm; eps as in pq1_norm_rope. */
+typedef struct {
+    const float* q_weight;
+    const float* k_weight;
+    float eps;
+} pq1_head_norm;
+
+/* pq1_kv_append with norms before the rotation, in the same launch (norm NULL:
+ * pq1_kv_append). */
+pq1_status pq1_kv_append_ex(const pq1_heads* k, const pq1_heads* v, const int64_t* slots,
+                            const pq1_heads* q, const pq1_heads* q_out, int32_t Hq,
+                            const int32_t* positions, const double* freqs,
+                            const pq1_rope_spec* spec, const pq1_head_norm* norm,
+                            const pq1_kv_cache* cache, int64_t T, void* stream);
+
+/* A paged cache of 4-bit numbers (the OCP MX format with e2m1 elements).  k and v
+ * are [pages][heads][page_size][dim / 2] bytes, two codes in each, the first in
+ * the low half; a code is a sign (bit 3) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ * k_scale and v_scale are [pages][heads][page_size][dim / 32] bytes: byte b
+ * multiplies the 32 codes of its group by 2^(b - 127); 255 makes them NaN.
+ * All contiguous and 16-byte aligned.  dtype, bf16 or f16, is the type of the
+ * queries and the one that values are read in: the append gives scales from
+ * 2^-100 to 2^125 (bf16) or 2^-23 to 2^13 (f16), with which every value is a finite
+ * number of that type, exactly.  page_size as in pq1_kv_cache; dim is a multiple
+ * of 32 up to 1024; heads up to 1024. */
+typedef struct {
+    void* k;
+    void* k_scale;
+    void* v;
+    void* v_scale;
+    int32_t dtype;
+    int32_t page_size;
+    int64_t pages;
+    int32_t heads;
+    int32_t dim;
+} pq1_kv4_cache;
+
+/* pq1_kv_append_ex into a 4-bit cache (norm may be NULL): arguments as there.
+ * A group's scale is the least power of two, within the range above, of which its
+ * largest magnitude is at most seven times; each value becomes the nearest
+ * multiple that a code stands for (ties to even codes), past six times the scale
+ * six times.  So the largest is off by half a step at most, but for f16 caches
+ * past 57344 and bf16 ones past 1.75 * 2^127.  A group with an infinity or NaN
+ * reads back as NaN.  Norms and rotations of keys are in fp64 up to the code, which
+ * is that of the formula's value unless it is within a few 2^-53 (or what the
+ * angle's own rounding moves it by) of the border between two. */
+pq1_status pq1_kv4_append(const pq1_heads* k, const pq1_heads* v, const int64_t* slots,
+                          const pq1_heads* q, const pq1_heads* q_out, int32_t Hq,
+                          const int32_t* positions, const double* freqs,
+                          const pq1_rope_spec* spec, const pq1_head_norm* norm,
+                          const pq1_kv4_cache* cache, int64_t T, void* stream);
+
+/* Rows of a 4-bit cache as numbers: token t of k_out and v_out ([T][heads][dim]
+ * views of one type, any of the three; either may be NULL) is row slots[t] of
+ * every head.  Slots may repeat; one outside the cache gives zeros.  Values are
+ * exact (scales outside the append's range may round, or give infinities, in
+ * two-byte types). */
+pq1_status pq1_kv4_read(const pq1_kv4_cache* cache, const int64_t* slots, const pq1_heads* k_out,
+                        const pq1_heads* v_out, int64_t T, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* pq1_status_str(pq1_status s);
 
