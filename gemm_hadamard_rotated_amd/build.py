@@ -43,15 +43,19 @@ ARCH = "gfx950"
 
 SOURCES = ["api.hip", "rotate.hip", "gemv.hip", "gemv_packed.hip", "gemm.hip", "gemm_skinny.hip",
            "api_attention.hip", "rope.hip", "paged_attention.hip",
-           "paged_attention_tiles.hip", "api_kv4.hip", "norm_rope.hip", "kv4_read.hip"]
+           "paged_attention_tiles.hip", "paged_attention_sinks.hip",
+           "paged_attention_tiles_sinks.hip", "api_kv4.hip", "norm_rope.hip", "kv4_read.hip",
+           "kv4_attention.hip", "kv4_attention_tiles.hip"]
 BENCH_SOURCES = ["bench_kernels.hip"]
 
 # gemm_skinny.hip: MFMA results stay in ordinary VGPRs (the per-group fold
 # reads them right away; the accumulator-register form cost a copy each).
-# paged_attention_tiles.hip: likewise, scores and outputs are read by the softmax.
-SOURCE_FLAGS: dict = {"gemm_skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-                      "paged_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-                      "paged_attention_tiles.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# The attention kernels: likewise, scores and outputs are read by the softmax.
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+SOURCE_FLAGS: dict = {src: _VGPR_FORM for src in
+                      ("gemm_skinny.hip", "paged_attention.hip", "paged_attention_tiles.hip",
+                       "paged_attention_sinks.hip", "paged_attention_tiles_sinks.hip",
+                       "kv4_attention.hip", "kv4_attention_tiles.hip")}
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=fast",

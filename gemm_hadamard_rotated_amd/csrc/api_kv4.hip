@@ -9,11 +9,6 @@ using namespace pq1;
 
 namespace {
 
-struct Range {
-  const void* p;
-  size_t n;
-};
-
 bool meets(const Range& a, const Range& b) { return overlaps(a.p, a.n, b.p, b.n); }
 
 bool same_view(const pq1_heads& a, const pq1_heads& b) {
@@ -33,24 +28,6 @@ void add_angles(Range* in, int* n, const pq1_rope_spec* spec, const int32_t* pos
   if (spec == nullptr) return;
   in[(*n)++] = {positions, static_cast<size_t>(spec->axes) * T * 4};
   in[(*n)++] = {freqs, static_cast<size_t>(spec->rot) * 4};
-}
-
-pq1_status check_cache4(const pq1_kv4_cache& c) {
-  const pq1_kv_cache sizes{c.k, c.v, c.dtype, c.page_size, c.pages, c.heads, c.dim};
-  if (pq1_status st = check_cache(sizes); st != PQ1_OK) return st;
-  if (c.dim % 32 != 0) return PQ1_ERR_SHAPE;
-  if (c.k_scale == nullptr || c.v_scale == nullptr) return PQ1_ERR_NULL;
-  if (!aligned16(c.k_scale) || !aligned16(c.v_scale)) return PQ1_ERR_ALIGN;
-  return PQ1_OK;
-}
-
-// The four arrays of a cache.
-void ranges_of(const pq1_kv4_cache& c, Range (&r)[4]) {
-  const size_t rows = static_cast<size_t>(c.pages) * c.page_size * c.heads;
-  r[0] = {c.k, rows * (c.dim / 2)};
-  r[1] = {c.v, rows * (c.dim / 2)};
-  r[2] = {c.k_scale, rows * (c.dim / 32)};
-  r[3] = {c.v_scale, rows * (c.dim / 32)};
 }
 
 // What both appends check and pass on; `out` holds the cache's arrays.

@@ -129,4 +129,28 @@ inline pq1_status check_attention_sizes(int64_t B, int64_t T, int64_t Hq, int64_
   return PQ1_OK;
 }
 
+// Memory of an argument.
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+inline pq1_status check_cache4(const pq1_kv4_cache& c) {
+  const pq1_kv_cache sizes{c.k, c.v, c.dtype, c.page_size, c.pages, c.heads, c.dim};
+  if (pq1_status st = check_cache(sizes); st != PQ1_OK) return st;
+  if (c.dim % 32 != 0) return PQ1_ERR_SHAPE;
+  if (c.k_scale == nullptr || c.v_scale == nullptr) return PQ1_ERR_NULL;
+  if (!aligned16(c.k_scale) || !aligned16(c.v_scale)) return PQ1_ERR_ALIGN;
+  return PQ1_OK;
+}
+
+// The four arrays of a cache.
+inline void ranges_of(const pq1_kv4_cache& c, Range* r) {
+  const size_t rows = static_cast<size_t>(c.pages) * c.page_size * c.heads;
+  r[0] = {c.k, rows * (c.dim / 2)};
+  r[1] = {c.v, rows * (c.dim / 2)};
+  r[2] = {c.k_scale, rows * (c.dim / 32)};
+  r[3] = {c.v_scale, rows * (c.dim / 32)};
+}
+
 }  // namespace pq1

@@ -113,11 +113,27 @@ struct AttnArgs {
   float scale_log2 = 0;  // scale * log2(e): the softmax runs in powers of two
   bool causal = false;
   int window = 0;
+  int sinks = 0;  // first keys that a window leaves visible
+  const uint8_t* k_scale = nullptr;  // of a 4-bit cache
+  const uint8_t* v_scale = nullptr;
 };
+
+// What the kernels attend over: pages of two-byte numbers; the same in windows
+// whose first keys stay visible; or pages of 4-bit numbers, with or without such
+// a window.
+enum CacheForm { kTwoByte, kTwoByteSinks, kFourBit };
 
 hipError_t launch_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
                             void* workspace, hipStream_t s);
 hipError_t launch_attention(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
                             void* workspace, hipStream_t s);
+hipError_t launch_sinks_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype,
+                                  int out_dtype, void* workspace, hipStream_t s);
+hipError_t launch_sinks_attention(const AttnPlan& plan, const AttnArgs& a, int dtype,
+                                  int out_dtype, void* workspace, hipStream_t s);
+hipError_t launch_kv4_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
+                                void* workspace, hipStream_t s);
+hipError_t launch_kv4_attention(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
+                                void* workspace, hipStream_t s);
 
 }  // namespace pq1

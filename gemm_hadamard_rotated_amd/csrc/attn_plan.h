@@ -44,12 +44,29 @@ inline bool prefer_many(int64_t units, int64_t rows, int64_t keys, int D) {
 // 14.6; at D = 128 700 keys 10.8 and 14.5, 1500 keys 16.7 and 14.7.
 constexpr int64_t kShort = 98304;
 
+// Parts of that many keys for so many (sequence, cache head, row tile)s.
+inline int64_t parts_of(bool many, int64_t units, int64_t keys, int D) {
+  constexpr int64_t cus = 256, step = kKeys * kWaves;
+  int64_t parts = 1;
+  if (many) {
+    // One workgroup to a CU: as many parts as the device takes at once.
+    // More, to even out a last round, cost more than they give (192
+    // workgroups of 7168 keys: 396 us; in 4 parts, three full rounds: 407 us
+    // and 48 to join them): idle CUs leave the others a higher clock.
+    while (units * (parts + 1) <= cus && (parts + 1) * 256 <= keys) ++parts;
+  } else if (units < cus && keys * D > kShort) {
+    parts = (cus + units - 1) / units;
+  }
+  // no part shorter than one key tile for each wave
+  const int64_t most_parts = (keys + step - 1) / step;
+  return parts < most_parts ? parts : most_parts;
+}
+
 inline AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_q,
                                int64_t max_kv, int window = 0) {
   // A launch holds less than 2^32 threads.  Kernels walk on over rows that
   // their grid has no workgroup for, so a long chunk only costs balance.
   constexpr int64_t most = (int64_t{1} << 32) / (2 * kTileRows) - 1;
-  constexpr int64_t cus = 256;
   AttnPlan p;
   if (B * Hk > most) return p;
   p.fits = true;
@@ -63,21 +80,7 @@ inline AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int6
   if (p.row_tiles > most / (B * Hk)) p.row_tiles = most / (B * Hk);
   const int64_t units = B * Hk * p.row_tiles;
   const int64_t step = kKeys * kWaves;
-  auto cut = [&](int64_t keys) {  // parts of that many keys
-    int64_t parts = 1;
-    if (p.many) {
-      // One workgroup to a CU: as many parts as the device takes at once.
-      // More, to even out a last round, cost more than they give (192
-      // workgroups of 7168 keys: 396 us; in 4 parts, three full rounds: 407 us
-      // and 48 to join them): idle CUs leave the others a higher clock.
-      while (units * (parts + 1) <= cus && (parts + 1) * 256 <= keys) ++parts;
-    } else if (units < cus && keys * D > kShort) {
-      parts = (cus + units - 1) / units;
-    }
-    // no part shorter than one key tile for each wave
-    const int64_t most_parts = (keys + step - 1) / step;
-    return parts < most_parts ? parts : most_parts;
-  };
+  auto cut = [&](int64_t keys) { return parts_of(p.many, units, keys, D); };
   // The workspace is for all keys, of which a window may leave fewer (a tile's
   // rows see the window's keys, one more for each row after the first, and the
   // start is rounded down): no more parts, shorter ones.
@@ -91,6 +94,41 @@ inline AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hk, int D, int6
   const int64_t n = cut(kv);
   p.chunk = static_cast<int>(((kv + n - 1) / n + step - 1) / step * step);
   p.nsplit = static_cast<int>((kv + p.chunk - 1) / p.chunk);
+  return p;
+}
+
+// The same for the calls whose workspace knows the window: the kernel is chosen,
+// and the workspace made, by the keys that a tile of rows walks over (with
+// `sinks` first keys that stay visible).
+inline AttnPlan plan_window(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t max_q,
+                            int64_t max_kv, int window, int sinks, bool four) {
+  constexpr int64_t most = (int64_t{1} << 32) / (2 * kTileRows) - 1;
+  AttnPlan p;
+  if (B * Hk > most) return p;
+  p.fits = true;
+  p.tokens = max_q < 1 ? 1 : max_q < T ? max_q : T;
+  const int64_t G = Hq / Hk, rows = p.tokens * G;
+  const int64_t kv = max_kv < 1 ? 1 : max_kv > kMaxKeys ? kMaxKeys : max_kv;
+  auto walk = [&](int64_t tile_rows) {
+    // the window of its first row, a key more for each token after that, the
+    // rounding of the start, and the first keys, rounded up
+    const int64_t tokens = (tile_rows + G - 1) / G + 1;
+    const int64_t reach = int64_t{window} + (tokens < p.tokens ? tokens : p.tokens) - 1 + 63 +
+                          (int64_t{sinks} + 63) / 64 * 64;
+    return window > 0 && reach < kv ? reach : kv;
+  };
+  static_cast<void>(four);
+  p.many = prefer_many(B * Hk, rows, walk(kTileRows), D);
+  p.tile_rows = p.many ? kTileRows : rows <= 16 ? 16 : 32;
+  p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+  if (p.row_tiles > most / (B * Hk)) p.row_tiles = most / (B * Hk);
+  const int64_t units = B * Hk * p.row_tiles;
+  const int64_t keys = walk(p.tile_rows), step = kKeys * kWaves;
+  const int64_t n = parts_of(p.many, units, keys, D);
+  p.chunk = static_cast<int>(((keys + n - 1) / n + step - 1) / step * step);
+  p.nsplit = static_cast<int>((keys + p.chunk - 1) / p.chunk);
+  p.workspace_bytes =
+      p.nsplit > 1 ? static_cast<size_t>(p.nsplit) * T * Hq * (D * 4 + 8) : 0;
   return p;
 }
 

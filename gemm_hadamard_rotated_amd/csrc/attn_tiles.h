@@ -6,6 +6,7 @@
 
 #include "attn_device.h"
 #include "attn_internal.h"
+#include "kv4_format.h"
 
 namespace pq1 {
 
@@ -47,17 +48,29 @@ __device__ __forceinline__ void visible(const AttnArgs& a, const Seq& s, int i, 
 // tokens i and the G query heads of the cache head, so that all of them share
 // the keys and values a workgroup reads.  A tile of such rows sees keys
 // [start, hi); they are cut into parts of `chunk` keys.
+//
+// In windows whose first `sinks` keys stay visible a tile walks over those and
+// then over the window: place w of its walk [start, end) is key w up to sink_end,
+// and key w + jump past it.  Both are multiples of 64, so that a tile of keys has
+// no jump inside.  Elsewhere places are keys.
 struct Parts {
-  int start;  // rounded down to a multiple of 32
-  int lo, hi;  // keys that some row sees
+  int start;  // rounded down to a multiple of 32 (64 with sinks)
+  int end;
+  int lo, hi;  // keys that some row sees (and the first ones)
   int lo_max, hi_min;  // keys in [lo_max, hi_min) are seen by every row
   int chunk;
+  int sink_end, jump;
   __device__ __forceinline__ int count() const {
-    const uint32_t keys = hi > start ? hi - start : 0;
+    const uint32_t keys = end > start ? end - start : 0;
     return static_cast<int>((keys + chunk - 1) / static_cast<uint32_t>(chunk));
+  }
+  template <CacheForm F>
+  __device__ __forceinline__ int key_at(int w) const {
+    return F == kTwoByte ? w : w < sink_end ? w : w + jump;
   }
 };
 
+template <CacheForm F>
 __device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int r0, int rows,
                                             int chunk, int nsplit) {
   const int last = s.n * a.G - 1;
@@ -67,25 +80,37 @@ __device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int
   visible(a, s, i0, &lo0, &hi0);
   visible(a, s, i1, &lo1, &hi1);
   p.start = lo0 & ~31;
+  p.end = hi1;
   p.lo = lo0;
   p.hi = hi1;
+  if constexpr (F != kTwoByte) {
+    const int first = lo0 & ~63;  // of the window
+    const int sinks = a.sinks < kMaxKeys ? a.sinks : kMaxKeys;
+    p.sink_end = (sinks + 63) & ~63;
+    p.jump = first > p.sink_end ? first - p.sink_end : 0;
+    p.start = 0;
+    p.end = hi1 - p.jump;
+  }
   p.lo_max = lo1;
   p.hi_min = hi0;
   p.chunk = chunk;
   // A cache longer than the caller said stretches the parts, to whole key tiles
   // of either kernel as the plan's are: a part's last tile has no keys of the next.
   const int64_t room = static_cast<int64_t>(chunk) * nsplit;
-  if (static_cast<int64_t>(p.hi) - p.start > room) {
+  if (static_cast<int64_t>(p.end) - p.start > room) {
     constexpr uint32_t step = kKeys * kWaves;
-    const uint32_t need = (static_cast<uint32_t>(p.hi - p.start) + nsplit - 1) / nsplit;
+    const uint32_t need = (static_cast<uint32_t>(p.end - p.start) + nsplit - 1) / nsplit;
     p.chunk = static_cast<int>((need + step - 1) / step * step);
   }
   return p;
 }
 
 // A tile of keys that not every row sees whole, or with a key on no page.
-__device__ __forceinline__ bool is_edge(const Parts& pt, int j0, int keys, bool gone) {
-  return j0 < pt.lo_max || j0 + keys > pt.hi_min || gone;
+template <CacheForm F>
+__device__ __forceinline__ bool is_edge(const AttnArgs& a, const Parts& pt, int j0, int keys,
+                                        bool gone) {
+  const bool cut = F == kTwoByte ? j0 < pt.lo_max : j0 < pt.lo_max && j0 + keys > a.sinks;
+  return cut || j0 + keys > pt.hi_min || gone;
 }
 
 template <typename T>
@@ -250,40 +275,52 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
 // rows [r0, r0 + count) of one (sequence, cache head), keys [k0, k1) in tiles
 // of `keys`.  Every thread of the workgroup calls it, after a barrier that
 // follows the stores.
-template <typename T, typename TO>
+template <typename T, typename TO, CacheForm F>
 __device__ __forceinline__ void put_back(const AttnArgs& a, const Seq& s, const int32_t* table,
                                          int h, const Parts& pt, int k0, int k1, int keys,
                                          int64_t r0, int count, int threads, int split,
                                          bool partial, float* part_o) {
   const int lane = threadIdx.x & 63;
   const int Hq = a.Hk * a.G;
-  for (int j0 = k0; j0 < k1; j0 += keys) {
-    const int j = j0 + lane < k1 ? j0 + lane : k1 - 1;
+  for (int w0 = k0; w0 < k1; w0 += keys) {
+    const int j0 = pt.key_at<F>(w0);
+    const int j = pt.key_at<F>(w0 + lane < k1 ? w0 + lane : k1 - 1);
     const int p = j >> a.page_shift;
     int page = p < a.max_pages ? table[p] : -1;
     if (page >= a.pages) page = -1;
-    if (!is_edge(pt, j0, keys, __any(page < 0 && lane < keys))) continue;
-    for (int key = 0; key < keys && j0 + key < k1; ++key) {
+    if (!is_edge<F>(a, pt, j0, keys, __any(page < 0 && lane < keys))) continue;
+    for (int key = 0; key < keys && w0 + key < k1; ++key) {
       const int pg = __shfl(page, key);
       if (pg < 0) continue;
-      const T* src = static_cast<const T*>(a.v_cache) +
-                     (((static_cast<int64_t>(pg) * a.Hk + h) << a.page_shift) +
-                      ((j0 + key) & ((1 << a.page_shift) - 1))) * a.D;
+      const int64_t row = ((static_cast<int64_t>(pg) * a.Hk + h) << a.page_shift) +
+                          ((j0 + key) & ((1 << a.page_shift) - 1));
       for (int e = threadIdx.x; e < count * a.D; e += threads) {
         const int64_t r = r0 + e / a.D;
         const int d = e % a.D;
-        const float x = static_cast<float>(src[d]);
+        float x;
+        if constexpr (F == kFourBit) {
+          // a group that the kernels took out holds NaN or infinities
+          const uint32_t byte = a.v_scale[row * (a.D / kGroup4) + d / kGroup4];
+          if (byte <= kMostExp<T> + 127) continue;
+          const uint32_t codes = static_cast<const uint8_t*>(a.v_cache)[row * (a.D / 2) + d / 2];
+          const uint32_t pair = pair_of<T, 0>(codes, scale_of(byte));
+          const uint16_t bits = static_cast<uint16_t>(pair >> 16 * (d % 2));
+          x = static_cast<float>(__builtin_bit_cast(T, bits));
+        } else {
+          x = static_cast<float>(static_cast<const T*>(a.v_cache)[row * a.D + d]);
+        }
         if (r >= static_cast<int64_t>(s.n) * a.G || __builtin_isfinite(x)) continue;
         const int i = a.by_G.div(static_cast<uint32_t>(r));
         int lo, hi;
         visible(a, s, i, &lo, &hi);
-        if (j0 + key < lo || j0 + key >= hi) continue;
-        const int64_t row = s.q0 + i;
+        const bool sink = F != kTwoByte && j0 + key < a.sinks;
+        if ((j0 + key < lo && !sink) || j0 + key >= hi) continue;
+        const int64_t token = s.q0 + i;
         const int hq = h * a.G + static_cast<int>(r) - i * a.G;
         if (partial) {
-          part_o[((split * a.T + row) * Hq + hq) * a.D + d] += x;
+          part_o[((split * a.T + token) * Hq + hq) * a.D + d] += x;
         } else {
-          TO* y = static_cast<TO*>(a.out) + row * a.o_ts + hq * a.o_hs + d;
+          TO* y = static_cast<TO*>(a.out) + token * a.o_ts + hq * a.o_hs + d;
           *y = static_cast<TO>(static_cast<float>(*y) + x);
         }
       }

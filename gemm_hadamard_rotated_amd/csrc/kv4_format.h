@@ -31,6 +31,16 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t codes, float scale) {
     return __builtin_bit_cast(uint32_t,
                               __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, SEL));
 }
+// The same with a byte number that unrolling makes a constant.
+template <typename T>
+__device__ __forceinline__ uint32_t pair_at(uint32_t codes, float scale, int sel) {
+  switch (sel) {
+    case 0: return pair_of<T, 0>(codes, scale);
+    case 1: return pair_of<T, 1>(codes, scale);
+    case 2: return pair_of<T, 2>(codes, scale);
+    default: return pair_of<T, 3>(codes, scale);
+  }
+}
 // Eight codes as four pairs.
 template <typename T>
 __device__ __forceinline__ void pairs_of(uint32_t codes, float scale, uint32_t (&out)[4]) {

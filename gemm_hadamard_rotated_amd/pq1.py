@@ -42,7 +42,9 @@ EXPORTS = ("pq1_rotate", "pq1_gemv_workspace_bytes", "pq1_gemv", "pq1_gemv_ex",
            "pq1_rotate_gemv_packed_noalloc", "pq1_rope", "pq1_kv_append",
            "pq1_paged_attention", "pq1_paged_attention_workspace_bytes", "pq1_norm_rope",
            "pq1_norm_rope_grad", "pq1_norm_rope_grad_workspace_bytes", "pq1_kv_append_ex",
-           "pq1_kv4_append", "pq1_kv4_read")
+           "pq1_kv4_append", "pq1_kv4_read", "pq1_paged_attention_ex",
+           "pq1_paged_attention_ex_workspace_bytes", "pq1_kv4_attention",
+           "pq1_kv4_attention_workspace_bytes")
 
 
 class Pq1Error(RuntimeError):
@@ -135,6 +137,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "pq1_kv_append_ex": (I32, [PH, PH, P, PH, PH, I32, P, P, PS, PN, PC, I64, P]),
             "pq1_kv4_append": (I32, [PH, PH, P, PH, PH, I32, P, P, PS, PN, P4, I64, P]),
             "pq1_kv4_read": (I32, [P4, P, PH, PH, I64, P]),
+            "pq1_paged_attention_ex": (I32, [PH, PH, PC, P, I64, P, P, I64, I64, I32, I64, I64, F,
+                                             I32, I32, I32, P, SZ, P]),
+            "pq1_paged_attention_ex_workspace_bytes": (SZ, [I64, I64, I32, I32, I32, I64, I64, I32,
+                                                            I32]),
+            "pq1_kv4_attention": (I32, [PH, PH, P4, P, I64, P, P, I64, I64, I32, I64, I64, F, I32,
+                                        I32, I32, P, SZ, P]),
+            "pq1_kv4_attention_workspace_bytes": (SZ, [I64, I64, I32, I32, I32, I64, I64, I32, I32]),
             "pq1_status_str": (ctypes.c_char_p, [I32]),
             "pq1_abi_version": (I32, []),
             "pq1_last_hip_error": (I32, []),
@@ -1215,21 +1224,10 @@ def _hints_and_window(max_q: int, max_kv: int, window: int):
     return hint(max_q), hint(max_kv), max(-1, min(window, 0x7fffffff))
 
 
-def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
-                        cu_q: torch.Tensor, kv_len: torch.Tensor, max_q: int, max_kv: int,
-                        scale: Optional[float] = None, causal: bool = True, window: int = 0,
-                        out: Optional[torch.Tensor] = None,
-                        out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
-    """Attention of the new tokens q [T][Hq][dim] of B sequences over the
-    cache (include/pq1.h, pq1_paged_attention).
-
-    page_table [B][max_pages], cu_q [B+1] and kv_len [B] are int32 on the GPU;
-    max_q and max_kv are the longest chunk and kv_len, known on the host.
-    scale defaults to dim^-0.5.  out (of q's type, or fp32) is new unless
-    given; rows that no sequence owns keep what they held.  The workspace is the
-    binding's: one for each stream, and one in each graph's own memory."""
-    if not isinstance(cache, KVCache):
-        raise TypeError("cache must be a KVCache")
+def _attention_arguments(q, cache, page_table, cu_q, kv_len, max_q, max_kv, scale, causal, window,
+                         out, out_dtype):
+    """What the attention calls check; their result and the C calls' arguments up to
+    the window."""
     dev, dt = cache.device, cache.dtype
     qv, size = _need_heads(q, "q", (dt,), dev)
     T, Hq, D = size
@@ -1257,18 +1255,73 @@ def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tenso
             raise TypeError(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
         ov, out_size = _need_heads(out, "out", (dt, torch.float32), dev)
         _same(out_size, size, "out")
-    lib = _lib or load_library()
     max_q, max_kv, window = int(max_q), int(max_kv), int(window)
     if max_q >> 62 or max_kv >> 62 or window >> 31:
         max_q, max_kv, window = _hints_and_window(max_q, max_kv, window)
-    args = (qv, ov, cache._struct, table, max_pages, cu, lens, B, T, Hq, max_q, max_kv,
-            D ** -0.5 if scale is None else float(scale), 1 if causal else 0, window)
-    if _current_device() == dev.index:
+    return out, (qv, ov, cache._struct, table, max_pages, cu, lens, B, T, Hq, max_q, max_kv,
+                 D ** -0.5 if scale is None else float(scale), 1 if causal else 0, window)
+
+
+def pq1_paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
+                        cu_q: torch.Tensor, kv_len: torch.Tensor, max_q: int, max_kv: int,
+                        scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                        out: Optional[torch.Tensor] = None,
+                        out_dtype: Optional[torch.dtype] = None, sinks: int = 0) -> torch.Tensor:
+    """Attention of the new tokens q [T][Hq][dim] of B sequences over the
+    cache (include/pq1.h, pq1_paged_attention).
+
+    page_table [B][max_pages], cu_q [B+1] and kv_len [B] are int32 on the GPU;
+    max_q and max_kv are the longest chunk and kv_len, known on the host.
+    scale defaults to dim^-0.5.  With a window the first `sinks` keys of a sequence
+    stay visible (pq1_paged_attention_ex).  out (of q's type, or fp32) is new unless
+    given; rows that no sequence owns keep what they held.  The workspace is the
+    binding's: one for each stream, and one in each graph's own memory."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    out, args = _attention_arguments(q, cache, page_table, cu_q, kv_len, max_q, max_kv, scale,
+                                     causal, window, out, out_dtype)
+    lib = _lib or load_library()
+    dev = cache.device
+    if sinks:
+        _attend_window(dev, "pq1_paged_attention_ex", lib.pq1_paged_attention_ex,
+                       lib.pq1_paged_attention_ex_workspace_bytes, cache, args, sinks)
+    elif _current_device() == dev.index:
         _attend(lib, dev, cache.heads, args)
     else:
         with torch.cuda.device(dev):
             _attend(lib, dev, cache.heads, args)
     return out
+
+
+def pq1_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tensor,
+                      cu_q: torch.Tensor, kv_len: torch.Tensor, max_q: int, max_kv: int,
+                      scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                      out: Optional[torch.Tensor] = None,
+                      out_dtype: Optional[torch.dtype] = None, sinks: int = 0) -> torch.Tensor:
+    """pq1_paged_attention over a 4-bit cache, q of its dtype: the same result as
+    over a cache that holds the values of pq1_kv4_read."""
+    if not isinstance(cache, KV4Cache):
+        raise TypeError("cache must be a KV4Cache")
+    out, args = _attention_arguments(q, cache, page_table, cu_q, kv_len, max_q, max_kv, scale,
+                                     causal, window, out, out_dtype)
+    lib = _lib or load_library()
+    _attend_window(cache.device, "pq1_kv4_attention", lib.pq1_kv4_attention,
+                   lib.pq1_kv4_attention_workspace_bytes, cache, args, sinks)
+    return out
+
+
+def _attend_window(dev, where: str, fn, need_of, cache, args, sinks: int) -> None:
+    sinks = int(sinks)
+    if sinks >> 31:  # past all lengths, or below zero, every number says the same
+        sinks = max(-1, min(sinks, 0x7fffffff))
+    args = (*args, sinks)
+    B, T, Hq, max_q, max_kv = args[7:12]
+    need = lambda: need_of(B, T, Hq, cache.heads, cache.dim, max_q, max_kv, args[14], sinks)
+    if _current_device() == dev.index:
+        _with_workspace(dev, where, fn, args, need)
+    else:
+        with torch.cuda.device(dev):
+            _with_workspace(dev, where, fn, args, need)
 
 
 def _attend(lib, dev, heads: int, args) -> None:

@@ -595,6 +595,36 @@ pq1_status pq1_kv4_append(const pq1_heads* k, const pq1_heads* v, const int64_t*
 pq1_status pq1_kv4_read(const pq1_kv4_cache* cache, const int64_t* slots, const pq1_heads* k_out,
                         const pq1_heads* v_out, int64_t T, void* stream);
 
+/* pq1_paged_attention in windows whose first keys stay visible: with window > 0
+ * the row at position p sees the keys j <= p with j > p - window or j < sinks.
+ *   sinks      >= 0; above 0 only with window > 0 (PQ1_ERR_ARG).
+ *   workspace  pq1_paged_attention_ex_workspace_bytes(...) bytes, as there; it
+ *              depends on window and sinks.
+ * Everything else as pq1_paged_attention. */
+pq1_status pq1_paged_attention_ex(const pq1_heads* q, const pq1_heads* out,
+                                  const pq1_kv_cache* cache, const int32_t* page_table,
+                                  int64_t max_pages, const int32_t* cu_q, const int32_t* kv_len,
+                                  int64_t B, int64_t T, int32_t Hq, int64_t max_q, int64_t max_kv,
+                                  float scale, int32_t causal, int32_t window, int32_t sinks,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+size_t pq1_paged_attention_ex_workspace_bytes(int64_t B, int64_t T, int32_t Hq, int32_t heads,
+                                              int32_t dim, int64_t max_q, int64_t max_kv,
+                                              int32_t window, int32_t sinks);
+
+/* The same over a 4-bit cache: what pq1_paged_attention_ex gives for a cache that
+ * holds the values of pq1_kv4_read, up to the order of sums.  q is of the cache's
+ * dtype, out of that type or fp32.  A group whose scale is 255 gives NaN in the rows
+ * that see it and no others; so may scales past the append's range. */
+pq1_status pq1_kv4_attention(const pq1_heads* q, const pq1_heads* out, const pq1_kv4_cache* cache,
+                             const int32_t* page_table, int64_t max_pages, const int32_t* cu_q,
+                             const int32_t* kv_len, int64_t B, int64_t T, int32_t Hq,
+                             int64_t max_q, int64_t max_kv, float scale, int32_t causal,
+                             int32_t window, int32_t sinks, void* workspace,
+                             size_t workspace_bytes, void* stream);
+size_t pq1_kv4_attention_workspace_bytes(int64_t B, int64_t T, int32_t Hq, int32_t heads,
+                                         int32_t dim, int64_t max_q, int64_t max_kv,
+                                         int32_t window, int32_t sinks);
+
 /* Static description of a status code (never NULL). */
 const char* pq1_status_str(pq1_status s);
 

@@ -36,6 +36,35 @@ def quantise(x, dtype):
     return y.flatten(-2), torch.where(fine, e + 127, 255.0).squeeze(-1).to(torch.uint8)
 
 
+def encode(y, byte):
+    """Codes [..., D / 2] of values that a cache with these scales holds."""
+    unit = torch.pow(torch.tensor(2.0, dtype=torch.float64), byte.double() - 127)
+    a = (y.abs().unflatten(-1, (-1, 32)) / unit.unsqueeze(-1)).flatten(-2)
+    code = (a.unsqueeze(-1) >= GRID[1:]).sum(-1) + 8 * torch.signbit(y)
+    return (code[..., 0::2] + 16 * code[..., 1::2]).to(torch.uint8)
+
+
+def attention(q, k, v, scale, causal, window, sinks):
+    """attention_reference.attention with the first `sinks` keys visible as well."""
+    q, k, v = q.double(), k.double(), v.double()
+    n, Hq, D = q.shape
+    kv, G = k.shape[0], Hq // k.shape[1]
+    o, weight, spread = torch.zeros_like(q), torch.zeros_like(q), 0.0
+    for i in range(n):
+        at = kv - n + i
+        seen = [j for j in range(kv) if not causal or (
+            j <= at and (not window or j > at - window or j < sinks))]
+        if not seen:
+            continue
+        for h in range(Hq):
+            K, V = k[seen, h // G], v[seen, h // G]
+            e = (K @ q[i, h]) * scale
+            spread = max(spread, float(((K.abs() @ q[i, h].abs()) * scale).nan_to_num(0, 0, 0).max()))
+            p = torch.softmax(e, dim=0)
+            o[i, h], weight[i, h] = p @ V, p @ V.abs()
+    return o, weight, spread
+
+
 def root(x, eps):
     """r of each head."""
     return (x.double().square().mean(-1, keepdim=True) + eps).rsqrt()
