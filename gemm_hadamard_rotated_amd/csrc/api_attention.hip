@@ -82,7 +82,7 @@ pq1_status attend(const AttnCall& c, const pq1_heads* q, const pq1_heads* out,
       (plan.workspace_bytes > 0 && overlaps(workspace, plan.workspace_bytes, out->data, ob)))
     return PQ1_ERR_ALIAS;
   if (pq1_status st = check_device(); st != PQ1_OK) return st;
-  AttnArgs a;
+  AttnWindowArgs a;
   a.q = q->data, a.q_ts = q->token_stride, a.q_hs = q->head_stride;
   a.out = out->data, a.o_ts = out->token_stride, a.o_hs = out->head_stride;
   a.k_cache = cache->k, a.v_cache = cache->v;
@@ -100,11 +100,12 @@ pq1_status attend(const AttnCall& c, const pq1_heads* q, const pq1_heads* out,
     a.k_scale = static_cast<const uint8_t*>(c.cache4->k_scale);
     a.v_scale = static_cast<const uint8_t*>(c.cache4->v_scale);
   }
-  const auto launch = c.form == kTwoByte        ? launch_attention
-                      : c.form == kTwoByteSinks ? launch_sinks_attention
-                                   : launch_kv4_attention;
-  return launched(
-      launch(plan, a, cache->dtype, out->dtype, workspace, static_cast<hipStream_t>(stream)));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (c.form == kTwoByte)
+    return launched(launch_attention(plan, a, cache->dtype, out->dtype, workspace, s));
+  if (c.form == kTwoByteSinks)
+    return launched(launch_sinks_attention(plan, a, cache->dtype, out->dtype, workspace, s));
+  return launched(launch_kv4_attention(plan, a, cache->dtype, out->dtype, workspace, s));
 }
 
 }  // namespace

@@ -86,7 +86,7 @@ __device__ __forceinline__ TileAt find_tile(const AttnArgs& a, const int32_t* ta
 // Both become pairs of T by one instruction for two codes.
 template <typename T, typename TO, int D, int RB, bool RUNS, CacheForm F>
 __global__ __launch_bounds__(64 * kWaves, D == 256 && (F != kFourBit || RB == 2) ? 1 : 2) void few_rows_kernel(
-    AttnArgs a, FewGrid fg, float* part_o, float2* part_ml) {
+    Args<F> a, FewGrid fg, float* part_o, float2* part_ml) {
   constexpr bool FOUR = F == kFourBit;
   constexpr int NP = kParts<T, TO>;
   // dimensions of V a lane reads at once
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 && (F != kFourBit || RB == 2)
       load_k(next, RUNS || wn < k1 ? jn : j0);
 
       if (is_edge<F>(a, pt, j0, kKeys, at.gone != 0)) {
-        const int sinks = a.sinks - j0 - 4 * g;
+        const int sinks = sinks_of<F>(a) - j0 - 4 * g;
         // Values no row sees become zero, and where rows see different keys
         // infinities and NaN among the others too (put_back).
         if (!RUNS || !one_token || j0 < pt.lo) {
@@ -502,7 +502,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 && (F != kFourBit || RB == 2)
     const bool put = !one_token && (odd_of[0] | odd_of[1] | odd_of[2] | odd_of[3]);
     __syncthreads();
     if (put) {
-      put_back<T, TO, F>(a, s, table, h, pt, k0, k1, kKeys, r0, ROWS, 64 * kWaves, split,
+      put_back_walk<T, TO, F>(a, s, table, h, pt, k0, k1, kKeys, r0, ROWS, 64 * kWaves, split,
                       fg.nsplit > 1, part_o);
       __syncthreads();
     }
@@ -514,7 +514,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 && (F != kFourBit || RB == 2)
 // maximum.  WPR waves share a row (each takes every WPR-th eight), D / 64
 // dimensions a lane.
 template <typename TO, int D, int WPR, bool SINKS>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, FewGrid fg, int tile_rows,
+__global__ __launch_bounds__(256) void join_kernel(Args<SINKS ? kTwoByteSinks : kTwoByte> a, FewGrid fg, int tile_rows,
                                                    int tokens, const float* part_o,
                                                    const float2* part_ml) {
   constexpr int N = D / 64, RPW = 4 / WPR, BATCH = 8;
@@ -612,7 +612,7 @@ FewGrid grid_of(const AttnPlan& plan, const AttnArgs& a) {
 }
 
 template <typename T, typename TO, int D, int RB, CacheForm F>
-hipError_t launch_few(const AttnPlan& plan, const AttnArgs& a, void* workspace, hipStream_t s) {
+hipError_t launch_few(const AttnPlan& plan, const Args<F>& a, void* workspace, hipStream_t s) {
   const FewGrid fg = grid_of(plan, a);
   float* part_o = static_cast<float*>(workspace);
   float2* part_ml =
@@ -626,8 +626,11 @@ hipError_t launch_few(const AttnPlan& plan, const AttnArgs& a, void* workspace, 
   return hipGetLastError();
 }
 
+template <bool SINKS>
+using JoinArgs = Args<SINKS ? kTwoByteSinks : kTwoByte>;
+
 template <typename TO, int D, int WPR, bool SINKS>
-hipError_t launch_join_waves(const AttnPlan& plan, const AttnArgs& a, void* workspace,
+hipError_t launch_join_waves(const AttnPlan& plan, const JoinArgs<SINKS>& a, void* workspace,
                              hipStream_t s) {
   const FewGrid fg = grid_of(plan, a);
   const float* part_o = static_cast<const float*>(workspace);
@@ -643,20 +646,20 @@ hipError_t launch_join_waves(const AttnPlan& plan, const AttnArgs& a, void* work
 }
 
 template <typename TO, int D, bool SINKS>
-hipError_t launch_join(const AttnPlan& plan, const AttnArgs& a, void* workspace, hipStream_t s) {
+hipError_t launch_join(const AttnPlan& plan, const JoinArgs<SINKS>& a, void* workspace, hipStream_t s) {
   // four waves to a row where there are several batches (64 parts: 9.1 -> 5.4 us)
   return plan.nsplit > 8 ? launch_join_waves<TO, D, 4, SINKS>(plan, a, workspace, s)
                          : launch_join_waves<TO, D, 1, SINKS>(plan, a, workspace, s);
 }
 
 template <typename T, typename TO, int D, CacheForm F>
-hipError_t launch_rows(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_rows(const AttnPlan& plan, const Args<F>& a, void* ws, hipStream_t s) {
   return plan.tile_rows == 16 ? launch_few<T, TO, D, 1, F>(plan, a, ws, s)
                               : launch_few<T, TO, D, 2, F>(plan, a, ws, s);
 }
 
 template <typename T, typename TO, CacheForm F>
-hipError_t launch_dims(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_dims(const AttnPlan& plan, const Args<F>& a, void* ws, hipStream_t s) {
   switch (a.D) {
     case 64: return launch_rows<T, TO, 64, F>(plan, a, ws, s);
     case 128: return launch_rows<T, TO, 128, F>(plan, a, ws, s);
@@ -665,7 +668,7 @@ hipError_t launch_dims(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStr
 }
 
 template <CacheForm F>
-hipError_t launch_few_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
+hipError_t launch_few_rows(const AttnPlan& plan, const Args<F>& a, int dtype, int out_dtype,
                            void* ws, hipStream_t s) {
   if (dtype == PQ1_BF16)
     return out_dtype == PQ1_F32 ? launch_dims<bf16, float, F>(plan, a, ws, s)
@@ -675,7 +678,7 @@ hipError_t launch_few_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, i
 }
 
 template <typename TO, bool SINKS>
-hipError_t join_dims(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStream_t s) {
+hipError_t join_dims(const AttnPlan& plan, const JoinArgs<SINKS>& a, void* ws, hipStream_t s) {
   switch (a.D) {
     case 64: return launch_join<TO, 64, SINKS>(plan, a, ws, s);
     case 128: return launch_join<TO, 128, SINKS>(plan, a, ws, s);
@@ -684,7 +687,7 @@ hipError_t join_dims(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStrea
 }
 
 template <bool SINKS>
-hipError_t join_parts(const AttnPlan& plan, const AttnArgs& a, int out_dtype, void* ws,
+hipError_t join_parts(const AttnPlan& plan, const JoinArgs<SINKS>& a, int out_dtype, void* ws,
                       hipStream_t s) {
   switch (out_dtype) {
     case PQ1_BF16: return join_dims<bf16, SINKS>(plan, a, ws, s);

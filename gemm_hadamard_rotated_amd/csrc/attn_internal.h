@@ -113,6 +113,11 @@ struct AttnArgs {
   float scale_log2 = 0;  // scale * log2(e): the softmax runs in powers of two
   bool causal = false;
   int window = 0;
+};
+
+// The same for the further forms.  (In AttnArgs these would cost the kernels that
+// do without them scalar registers: 2 % of a prompt chunk at D = 256.)
+struct AttnWindowArgs : AttnArgs {
   int sinks = 0;  // first keys that a window leaves visible
   const uint8_t* k_scale = nullptr;  // of a 4-bit cache
   const uint8_t* v_scale = nullptr;
@@ -122,18 +127,28 @@ struct AttnArgs {
 // whose first keys stay visible; or pages of 4-bit numbers, with or without such
 // a window.
 enum CacheForm { kTwoByte, kTwoByteSinks, kFourBit };
+template <CacheForm F>
+struct ArgsFor {
+  using type = AttnWindowArgs;
+};
+template <>
+struct ArgsFor<kTwoByte> {
+  using type = AttnArgs;
+};
+template <CacheForm F>
+using Args = typename ArgsFor<F>::type;
 
 hipError_t launch_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
                             void* workspace, hipStream_t s);
 hipError_t launch_attention(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
                             void* workspace, hipStream_t s);
-hipError_t launch_sinks_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype,
+hipError_t launch_sinks_many_rows(const AttnPlan& plan, const AttnWindowArgs& a, int dtype,
                                   int out_dtype, void* workspace, hipStream_t s);
-hipError_t launch_sinks_attention(const AttnPlan& plan, const AttnArgs& a, int dtype,
+hipError_t launch_sinks_attention(const AttnPlan& plan, const AttnWindowArgs& a, int dtype,
                                   int out_dtype, void* workspace, hipStream_t s);
-hipError_t launch_kv4_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
+hipError_t launch_kv4_many_rows(const AttnPlan& plan, const AttnWindowArgs& a, int dtype, int out_dtype,
                                 void* workspace, hipStream_t s);
-hipError_t launch_kv4_attention(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
+hipError_t launch_kv4_attention(const AttnPlan& plan, const AttnWindowArgs& a, int dtype, int out_dtype,
                                 void* workspace, hipStream_t s);
 
 }  // namespace pq1

@@ -112,7 +112,7 @@ constexpr int kTileWaves = kTileRows / 32;
 // into registers, a tile before they are wanted, and writes them to LDS as numbers of
 // T, where the products find them as they find copied ones.
 template <typename T, typename TO, int D, bool WIDE, CacheForm F>
-__global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, TileGrid tg,
+__global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, TileGrid tg,
                                                                     float* part_o,
                                                                     float2* part_ml) {
   constexpr int NP = kParts<T, TO>;
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
         const int r = at / PIECES;
         U4* v = reinterpret_cast<U4*>(vb + 16 * at);
         U4 x = *v;
-        const bool after = j0 + r >= pt.lo || (SINKS && j0 + r < a.sinks);
+        const bool after = j0 + r >= pt.lo || (SINKS && j0 + r < sinks_of<F>(a));
         const bool seen = after && j0 + r < pt.hi && !(gone >> r & 1);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -265,8 +265,10 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
         kc[n] = reinterpret_cast<const uint32_t*>(k)[n];
         vc[n] = reinterpret_cast<const uint32_t*>(v)[n];
       }
-      kscale = a.k_scale[sat];
-      vscale = a.v_scale[sat];
+      if constexpr (FOUR) {
+        kscale = a.k_scale[sat];
+        vscale = a.v_scale[sat];
+      }
     };
     // The tile at place w0 into LDS; in a tile's edge its values as `clean` leaves
     // them.
@@ -275,7 +277,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
       const int j0 = pt.key_at<F>(w0);
       if (is_edge<F>(a, pt, j0, KT, gone != 0)) {
         const int j = j0 + r;
-        const bool seen = (j >= pt.lo || j < a.sinks) && j < pt.hi && !(gone >> r & 1);
+        const bool seen = (j >= pt.lo || j < sinks_of<F>(a)) && j < pt.hi && !(gone >> r & 1);
         const bool take = seen && vscale <= kMostExp<T> + 127;
         odd4 |= seen && !take;
         vscale = take ? vscale : 127u;
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
         if (r < rows) visible(a, s, a.by_G.div(r), &lo, &hi);
         lo -= at;
         hi -= at;
-        const int sinks = a.sinks - at;
+        const int sinks = sinks_of<F>(a) - at;
 #pragma unroll
         for (int e = 0; e < EB; ++e)
 #pragma unroll
@@ -547,7 +549,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
     if constexpr (FOUR) odd_values = __syncthreads_or(odd4) != 0;
     if (odd_values) {
       __syncthreads();
-      put_back<T, TO, F>(a, s, table, h, pt, k0, k1, KT, r0, kTileRows, 64 * kTileWaves, split,
+      put_back_walk<T, TO, F>(a, s, table, h, pt, k0, k1, KT, r0, kTileRows, 64 * kTileWaves, split,
                       tg.nsplit > 1, part_o);
     }
     __syncthreads();  // the next tile of rows takes the buffers
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(AttnArgs a, 
 }
 
 template <typename T, typename TO, int D, CacheForm F>
-hipError_t launch_tiles(const AttnPlan& plan, const AttnArgs& a, void* workspace, hipStream_t s) {
+hipError_t launch_tiles(const AttnPlan& plan, const Args<F>& a, void* workspace, hipStream_t s) {
   const TileGrid tg{static_cast<int>(plan.row_tiles), plan.nsplit, plan.chunk};
   float* part_o = static_cast<float*>(workspace);
   float2* part_ml =
@@ -576,7 +578,7 @@ hipError_t launch_tiles(const AttnPlan& plan, const AttnArgs& a, void* workspace
 }
 
 template <typename T, typename TO, CacheForm F>
-hipError_t launch_dim(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_dim(const AttnPlan& plan, const Args<F>& a, void* ws, hipStream_t s) {
   switch (a.D) {
     case 64: return launch_tiles<T, TO, 64, F>(plan, a, ws, s);
     case 128: return launch_tiles<T, TO, 128, F>(plan, a, ws, s);
@@ -585,7 +587,7 @@ hipError_t launch_dim(const AttnPlan& plan, const AttnArgs& a, void* ws, hipStre
 }
 
 template <CacheForm F>
-hipError_t launch_types(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
+hipError_t launch_types(const AttnPlan& plan, const Args<F>& a, int dtype, int out_dtype,
                         void* ws, hipStream_t s) {
   if (dtype == PQ1_BF16)
     return out_dtype == PQ1_F32 ? launch_dim<bf16, float, F>(plan, a, ws, s)

@@ -71,7 +71,7 @@ struct Parts {
 };
 
 template <CacheForm F>
-__device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int r0, int rows,
+__device__ __forceinline__ Parts split_keys(const Args<F>& a, const Seq& s, int r0, int rows,
                                             int chunk, int nsplit) {
   const int last = s.n * a.G - 1;
   const int i0 = a.by_G.div(r0), i1 = a.by_G.div(r0 + rows - 1 < last ? r0 + rows - 1 : last);
@@ -105,12 +105,23 @@ __device__ __forceinline__ Parts split_keys(const AttnArgs& a, const Seq& s, int
   return p;
 }
 
+// First keys that every window leaves visible.
+template <CacheForm F>
+__device__ __forceinline__ int sinks_of(const Args<F>& a) {
+  if constexpr (F == kTwoByte)
+    return 0;
+  else
+    return a.sinks;
+}
+
 // A tile of keys that not every row sees whole, or with a key on no page.
 template <CacheForm F>
-__device__ __forceinline__ bool is_edge(const AttnArgs& a, const Parts& pt, int j0, int keys,
+__device__ __forceinline__ bool is_edge(const Args<F>& a, const Parts& pt, int j0, int keys,
                                         bool gone) {
-  const bool cut = F == kTwoByte ? j0 < pt.lo_max : j0 < pt.lo_max && j0 + keys > a.sinks;
-  return cut || j0 + keys > pt.hi_min || gone;
+  if constexpr (F == kTwoByte)
+    return j0 < pt.lo_max || j0 + keys > pt.hi_min || gone;
+  else
+    return (j0 < pt.lo_max && j0 + keys > a.sinks) || j0 + keys > pt.hi_min || gone;
 }
 
 template <typename T>
@@ -269,6 +280,24 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
   return pair & ~(b | (b - (b >> 15)));
 }
 
+// Element d of a row of V.  `row` counts elements of T from the cache's start, also
+// where the cache holds 4-bit ones: then what was not taken out of a tile, a group
+// of finite values, counts as zero.
+template <typename T, CacheForm F>
+__device__ __forceinline__ float value_at(const Args<F>& a, const T* row, int d) {
+  if constexpr (F == kFourBit) {
+    const int64_t at = row + d - static_cast<const T*>(a.v_cache);
+    const uint32_t byte = a.v_scale[at / kGroup4];
+    if (byte <= kMostExp<T> + 127) return 0.0f;
+    const uint32_t codes = static_cast<const uint8_t*>(a.v_cache)[at / 2];
+    const uint32_t pair = pair_of<T, 0>(codes, scale_of(byte));
+    const uint16_t bits = static_cast<uint16_t>(pair >> 16 * (at % 2));
+    return static_cast<float>(__builtin_bit_cast(T, bits));
+  } else {
+    return static_cast<float>(row[d]);
+  }
+}
+
 // Where the values of a tile's edge are not finite, both kernels take them for
 // zero, because times a probability of zero they would be NaN in the rows that
 // do not see them.  Here the rows that do see them add them to their results:
@@ -276,54 +305,64 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
 // of `keys`.  Every thread of the workgroup calls it, after a barrier that
 // follows the stores.
 template <typename T, typename TO, CacheForm F>
-__device__ __forceinline__ void put_back(const AttnArgs& a, const Seq& s, const int32_t* table,
+__device__ __forceinline__ void put_back(const Args<F>& a, const Seq& s, const int32_t* table,
                                          int h, const Parts& pt, int k0, int k1, int keys,
                                          int64_t r0, int count, int threads, int split,
                                          bool partial, float* part_o) {
   const int lane = threadIdx.x & 63;
   const int Hq = a.Hk * a.G;
-  for (int w0 = k0; w0 < k1; w0 += keys) {
-    const int j0 = pt.key_at<F>(w0);
-    const int j = pt.key_at<F>(w0 + lane < k1 ? w0 + lane : k1 - 1);
+  for (int j0 = k0; j0 < k1; j0 += keys) {
+    const int j = j0 + lane < k1 ? j0 + lane : k1 - 1;
     const int p = j >> a.page_shift;
     int page = p < a.max_pages ? table[p] : -1;
     if (page >= a.pages) page = -1;
     if (!is_edge<F>(a, pt, j0, keys, __any(page < 0 && lane < keys))) continue;
-    for (int key = 0; key < keys && w0 + key < k1; ++key) {
+    for (int key = 0; key < keys && j0 + key < k1; ++key) {
       const int pg = __shfl(page, key);
       if (pg < 0) continue;
-      const int64_t row = ((static_cast<int64_t>(pg) * a.Hk + h) << a.page_shift) +
-                          ((j0 + key) & ((1 << a.page_shift) - 1));
+      const T* src = static_cast<const T*>(a.v_cache) +
+                     (((static_cast<int64_t>(pg) * a.Hk + h) << a.page_shift) +
+                      ((j0 + key) & ((1 << a.page_shift) - 1))) * a.D;
       for (int e = threadIdx.x; e < count * a.D; e += threads) {
         const int64_t r = r0 + e / a.D;
         const int d = e % a.D;
-        float x;
-        if constexpr (F == kFourBit) {
-          // a group that the kernels took out holds NaN or infinities
-          const uint32_t byte = a.v_scale[row * (a.D / kGroup4) + d / kGroup4];
-          if (byte <= kMostExp<T> + 127) continue;
-          const uint32_t codes = static_cast<const uint8_t*>(a.v_cache)[row * (a.D / 2) + d / 2];
-          const uint32_t pair = pair_of<T, 0>(codes, scale_of(byte));
-          const uint16_t bits = static_cast<uint16_t>(pair >> 16 * (d % 2));
-          x = static_cast<float>(__builtin_bit_cast(T, bits));
-        } else {
-          x = static_cast<float>(static_cast<const T*>(a.v_cache)[row * a.D + d]);
-        }
+        const float x = value_at<T, F>(a, src, d);
         if (r >= static_cast<int64_t>(s.n) * a.G || __builtin_isfinite(x)) continue;
         const int i = a.by_G.div(static_cast<uint32_t>(r));
         int lo, hi;
         visible(a, s, i, &lo, &hi);
-        const bool sink = F != kTwoByte && j0 + key < a.sinks;
-        if ((j0 + key < lo && !sink) || j0 + key >= hi) continue;
-        const int64_t token = s.q0 + i;
+        if (F != kTwoByte && j0 + key < sinks_of<F>(a)) lo = 0;
+        if (j0 + key < lo || j0 + key >= hi) continue;
+        const int64_t row = s.q0 + i;
         const int hq = h * a.G + static_cast<int>(r) - i * a.G;
         if (partial) {
-          part_o[((split * a.T + token) * Hq + hq) * a.D + d] += x;
+          part_o[((split * a.T + row) * Hq + hq) * a.D + d] += x;
         } else {
-          TO* y = static_cast<TO*>(a.out) + token * a.o_ts + hq * a.o_hs + d;
+          TO* y = static_cast<TO*>(a.out) + row * a.o_ts + hq * a.o_hs + d;
           *y = static_cast<TO>(static_cast<float>(*y) + x);
         }
       }
+    }
+  }
+}
+
+// The same for places [w0, w1) of the tile's walk.
+template <typename T, typename TO, CacheForm F>
+__device__ __forceinline__ void put_back_walk(const Args<F>& a, const Seq& s, const int32_t* table,
+                                              int h, const Parts& pt, int w0, int w1, int keys,
+                                              int64_t r0, int count, int threads, int split,
+                                              bool partial, float* part_o) {
+  if constexpr (F == kTwoByte) {
+    put_back<T, TO, F>(a, s, table, h, pt, w0, w1, keys, r0, count, threads, split, partial, part_o);
+  } else {
+    // at most two runs of keys
+#pragma unroll 1
+    for (int first = w0; first < w1;) {
+      const int last = first < pt.sink_end && pt.sink_end < w1 ? pt.sink_end : w1;
+      const int j0 = pt.key_at<F>(first);
+      put_back<T, TO, F>(a, s, table, h, pt, j0, j0 + (last - first), keys, r0, count, threads,
+                         split, partial, part_o);
+      first = last;
     }
   }
 }

@@ -3,7 +3,7 @@
 
 namespace pq1 {
 
-hipError_t launch_kv4_many_rows(const AttnPlan& plan, const AttnArgs& a, int dtype, int out_dtype,
+hipError_t launch_kv4_many_rows(const AttnPlan& plan, const AttnWindowArgs& a, int dtype, int out_dtype,
                                 void* workspace, hipStream_t s) {
   return launch_types<kFourBit>(plan, a, dtype, out_dtype, workspace, s);
 }

@@ -4,7 +4,7 @@
 
 namespace pq1 {
 
-hipError_t launch_sinks_attention(const AttnPlan& plan, const AttnArgs& a, int dtype,
+hipError_t launch_sinks_attention(const AttnPlan& plan, const AttnWindowArgs& a, int dtype,
                                   int out_dtype, void* workspace, hipStream_t s) {
   const hipError_t e =
       plan.many ? launch_sinks_many_rows(plan, a, dtype, out_dtype, workspace, s)

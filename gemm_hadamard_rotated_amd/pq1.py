@@ -1183,12 +1183,13 @@ def pq1_norm_rope_grad(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
     dw = torch.empty_like(weight) if weight_grad else None
     args = (gv, xv, dv, w, dw.data_ptr() if weight_grad else None, eps, pos, freqs,
             spec[1 if inverse else 0], T, H, D)
-    need = lambda: lib.pq1_norm_rope_grad_workspace_bytes(T, D) if weight_grad else 0
+    call = (dev, "pq1_norm_rope_grad", lib.pq1_norm_rope_grad, args,
+            lib.pq1_norm_rope_grad_workspace_bytes, (T if weight_grad else 0, D))
     if _current_device() == dev.index:
-        _with_workspace(dev, "pq1_norm_rope_grad", lib.pq1_norm_rope_grad, args, need)
+        _with_workspace(*call)
     else:
         with torch.cuda.device(dev):
-            _with_workspace(dev, "pq1_norm_rope_grad", lib.pq1_norm_rope_grad, args, need)
+            _with_workspace(*call)
     return dx, dw
 
 
@@ -1316,25 +1317,25 @@ def _attend_window(dev, where: str, fn, need_of, cache, args, sinks: int) -> Non
         sinks = max(-1, min(sinks, 0x7fffffff))
     args = (*args, sinks)
     B, T, Hq, max_q, max_kv = args[7:12]
-    need = lambda: need_of(B, T, Hq, cache.heads, cache.dim, max_q, max_kv, args[14], sinks)
+    sizes = (B, T, Hq, cache.heads, cache.dim, max_q, max_kv, args[14], sinks)
     if _current_device() == dev.index:
-        _with_workspace(dev, where, fn, args, need)
+        _with_workspace(dev, where, fn, args, need_of, sizes)
     else:
         with torch.cuda.device(dev):
-            _with_workspace(dev, where, fn, args, need)
+            _with_workspace(dev, where, fn, args, need_of, sizes)
 
 
 def _attend(lib, dev, heads: int, args) -> None:
     _with_workspace(dev, "pq1_paged_attention", lib.pq1_paged_attention, args,
-                    lambda: _attention_workspace_bytes(lib, heads, args))
+                    _attention_workspace_bytes, (lib, heads, args))
 
 
-def _with_workspace(dev, where: str, fn, args, need_of) -> None:
+def _with_workspace(dev, where: str, fn, args, need_of, sizes) -> None:
     """The call with the stream's present workspace; only if the library
     refuses that is the size asked for (0.5 us a call)."""
     stream = _raw_stream(dev.index)
     if stream and _capturing():  # (the default stream cannot be captured)
-        need = need_of()
+        need = need_of(*sizes)
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         code = fn(*args, ws.data_ptr() if need else None, need, stream)
         if code != PQ1_OK:
@@ -1347,7 +1348,7 @@ def _with_workspace(dev, where: str, fn, args, need_of) -> None:
         if code == PQ1_OK:
             return
         if code in (1, 8):  # PQ1_ERR_NULL, PQ1_ERR_ARG: perhaps no workspace yet, or too small a one
-            need = need_of()
+            need = need_of(*sizes)
             if need > ws[2]:
                 ws = _grow_attention_workspace(key, need, dev)
                 code = fn(*args, ws[1], ws[2], stream)
