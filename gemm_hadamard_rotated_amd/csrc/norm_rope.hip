@@ -60,6 +60,13 @@ __device__ __forceinline__ float2 turn_of(int32_t pos, double freq, bool inverse
   sincospif(2.0f * static_cast<float>(turn), &s, &c);
   return make_float2(c, inverse ? -s : s);
 }
+// A constant that is made where it is used (out of the loops around it, the
+// series' constants would hold registers).
+__device__ __forceinline__ double just(double c) {
+  asm volatile("" : "+s"(c));
+  return c;
+}
+
 // In fp64: the angle less the nearest multiple n of pi / 2 (taken as the sum of two
 // numbers; the first difference is exact but for its last rounding, for n up to
 // 2^31 the second's share is below 2^-24), then the power series up to x^17 and x^16,
@@ -69,23 +76,23 @@ __device__ __forceinline__ double2 turn_of(int32_t pos, double freq, bool invers
   const double n = rint(angle * 0.63661977236758134);
   const double x = fma(-n, 6.123233995736766e-17, fma(-n, 1.5707963267948966, angle));
   const double z = x * x;
-  double s = 1.0 / 355687428096000.0, c = 1.0 / 20922789888000.0;
-  s = fma(s, z, -1.0 / 1307674368000.0);
-  c = fma(c, z, -1.0 / 87178291200.0);
-  s = fma(s, z, 1.0 / 6227020800.0);
-  c = fma(c, z, 1.0 / 479001600.0);
-  s = fma(s, z, -1.0 / 39916800.0);
-  c = fma(c, z, -1.0 / 3628800.0);
-  s = fma(s, z, 1.0 / 362880.0);
-  c = fma(c, z, 1.0 / 40320.0);
-  s = fma(s, z, -1.0 / 5040.0);
-  c = fma(c, z, -1.0 / 720.0);
-  s = fma(s, z, 1.0 / 120.0);
-  c = fma(c, z, 1.0 / 24.0);
-  s = fma(s, z, -1.0 / 6.0);
-  c = fma(c, z, -0.5);
+  double s = just(1.0 / 355687428096000.0), c = just(1.0 / 20922789888000.0);
+  s = fma(s, z, just(-1.0 / 1307674368000.0));
+  c = fma(c, z, just(-1.0 / 87178291200.0));
+  s = fma(s, z, just(1.0 / 6227020800.0));
+  c = fma(c, z, just(1.0 / 479001600.0));
+  s = fma(s, z, just(-1.0 / 39916800.0));
+  c = fma(c, z, just(-1.0 / 3628800.0));
+  s = fma(s, z, just(1.0 / 362880.0));
+  c = fma(c, z, just(1.0 / 40320.0));
+  s = fma(s, z, just(-1.0 / 5040.0));
+  c = fma(c, z, just(-1.0 / 720.0));
+  s = fma(s, z, just(1.0 / 120.0));
+  c = fma(c, z, just(1.0 / 24.0));
+  s = fma(s, z, just(-1.0 / 6.0));
+  c = fma(c, z, just(-0.5));
   s = fma(s * z, x, x);
-  c = fma(c, z, 1.0);
+  c = fma(c, z, just(1.0));
   const int quarter = static_cast<int>(n - 4.0 * floor(0.25 * n));
   const double cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
   const bool minus_c = quarter == 1 || quarter == 2, minus_s = (quarter >= 2) != inverse;
@@ -322,7 +329,8 @@ __host__ __device__ __forceinline__ constexpr int table_bytes(int pairs) {
 }
 
 template <typename TI, typename TO, int NB, Into INTO>
-__global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormArgs a, NormDims dm) {
+__global__ __launch_bounds__(kThreads, INTO == kCache4 && NB == 1 ? 4 : 1) void norm_rope_kernel(
+    NormArgs a, NormDims dm) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const RopeArgs& r = a.rope;
   const int half = r.rot >> 1;
@@ -495,7 +503,7 @@ hipError_t launch_heads(const NormArgs& a, hipStream_t s) {
   // as many workgroups as the device holds at once, by registers; four lanes are a
   // group of a 4-bit cache
   const uint32_t blocks = static_cast<uint32_t>(
-      cut_heads(&dm, r, heads, INTO == kCache4 ? 2 : 0, INTO == kCache4 ? 768 : 1024));
+      cut_heads(&dm, r, heads, INTO == kCache4 ? 2 : 0, 1024));
   const bool two = r.D / 8 > 64;
   const int exchange = half_exchange(r) ? kThreads * (two ? kLaneBytes<INTO, 2> : kLaneBytes<INTO, 1>)
                                         : 0;
