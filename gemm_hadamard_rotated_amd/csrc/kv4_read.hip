@@ -21,7 +21,6 @@ struct ReadDims {
   uint32_t tokens;    // tokens of the launch
 };
 
-template <typename TO>
 __device__ __forceinline__ void widen(uint32_t codes, uint32_t byte, float (&v)[8]) {
   using F2 = __attribute__((ext_vector_type(2))) float;
   const float s = scale_of(byte);
@@ -34,44 +33,72 @@ __device__ __forceinline__ void widen(uint32_t codes, uint32_t byte, float (&v)[
   for (int i = 0; i < 8; ++i) v[i] = p[i / 2][i % 2];
 }
 
-template <typename TO, int U>
-__global__ __launch_bounds__(kThreads) void kv4_read_kernel(Read4Args a, ReadDims dm) {
-  TO* dst[U];
-  uint32_t codes[U], byte[U];
+// PAST: past the caches.
+template <bool PAST, typename TO>
+__device__ __forceinline__ void store_eight(TO* dst, const float (&v)[8]) {
+  if constexpr (PAST) {
+    using U4 = __attribute__((ext_vector_type(4))) uint32_t;
+    constexpr int N = sizeof(TO) * 8 / 16;
+    struct Words {
+      U4 w[N];
+    };
+    Pack<TO, 8> r;
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const uint32_t u = (blockIdx.x * U + k) * kThreads + threadIdx.x;
-    const uint32_t tl = dm.per_token.div(u);
-    dst[k] = nullptr;
-    codes[k] = byte[k] = 0;
-    if (tl >= dm.tokens) continue;
-    const int64_t t = dm.first + tl;
-    uint32_t w = u - tl * dm.per_token.d;
-    const bool value = w >= static_cast<uint32_t>(dm.keys);
-    if (value) w -= dm.keys;
-    const uint32_t h = dm.per_head.div(w);
-    w -= h * dm.per_head.d;
-    // keys first, unless only values are wanted
-    const bool of_v = value || a.k_out == nullptr;
-    dst[k] = (of_v ? static_cast<TO*>(a.v_out) + t * a.v_ts + h * a.v_hs
-                   : static_cast<TO*>(a.k_out) + t * a.k_ts + h * a.k_hs) + 8 * w;
-    const int64_t slot = a.slots[t];
-    if (slot < 0 || slot >= a.slot_count) continue;
-    const int64_t page = slot >> a.page_shift;
-    const int64_t row = ((page * a.H + h) << a.page_shift) + (slot - (page << a.page_shift));
-    codes[k] = reinterpret_cast<const uint32_t*>((of_v ? a.v : a.k) + row * (a.D / 2))[w];
-    byte[k] = ((of_v ? a.v_scale : a.k_scale) + row * (a.D / kGroup4))[w / 4];
-  }
+    for (int i = 0; i < 8; ++i) r.e[i] = static_cast<TO>(v[i]);
+    const Words x = __builtin_bit_cast(Words, r);
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    if (dst[k] == nullptr) continue;
-    float v[8];
-    widen<TO>(codes[k], byte[k], v);
-    store_wide(dst[k], v);
+    for (int n = 0; n < N; ++n) __builtin_nontemporal_store(x.w[n], reinterpret_cast<U4*>(dst) + n);
+  } else {
+    store_wide(dst, v);
   }
 }
 
-template <typename TO, int U>
+template <typename TO, int U, bool PAST>
+__global__ __launch_bounds__(kThreads) void kv4_read_kernel(Read4Args a, ReadDims dm) {
+  // All slots are read, then all codes: two waits for memory in all.
+  uint32_t w[U], h[U], codes[U], byte[U];
+  int64_t t[U], slot[U];
+  bool mine[U], of_v[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const uint32_t u = (blockIdx.x * U + k) * kThreads + threadIdx.x;
+    uint32_t tl = dm.per_token.div(u);
+    w[k] = u - tl * dm.per_token.d;
+    mine[k] = tl < dm.tokens;
+    tl = mine[k] ? tl : 0;
+    t[k] = dm.first + tl;
+    slot[k] = a.slots[t[k]];
+    const bool value = w[k] >= static_cast<uint32_t>(dm.keys);
+    if (value) w[k] -= dm.keys;
+    h[k] = dm.per_head.div(w[k]);
+    w[k] -= h[k] * dm.per_head.d;
+    // keys first, unless only values are wanted
+    of_v[k] = value || a.k_out == nullptr;
+  }
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const bool stored = slot[k] >= 0 && slot[k] < a.slot_count;
+    const int64_t at = stored ? slot[k] : 0;
+    const int64_t page = at >> a.page_shift;
+    const int64_t row = ((page * a.H + h[k]) << a.page_shift) + (at - (page << a.page_shift));
+    const uint32_t c =
+        reinterpret_cast<const uint32_t*>((of_v[k] ? a.v : a.k) + row * (a.D / 2))[w[k]];
+    const uint32_t s = ((of_v[k] ? a.v_scale : a.k_scale) + row * (a.D / kGroup4))[w[k] / 4];
+    codes[k] = stored ? c : 0;
+    byte[k] = stored ? s : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    if (!mine[k]) continue;
+    TO* const dst = (of_v[k] ? static_cast<TO*>(a.v_out) + t[k] * a.v_ts + h[k] * a.v_hs
+                             : static_cast<TO*>(a.k_out) + t[k] * a.k_ts + h[k] * a.k_hs) + 8 * w[k];
+    float v[8];
+    widen(codes[k], byte[k], v);
+    store_eight<PAST>(dst, v);
+  }
+}
+
+template <typename TO, int U, bool PAST>
 hipError_t launch_units(const Read4Args& a, ReadDims dm, hipStream_t s) {
   // a launch holds less than 2^32 threads
   const int64_t per_token = dm.per_token.d;
@@ -79,7 +106,7 @@ hipError_t launch_units(const Read4Args& a, ReadDims dm, hipStream_t s) {
   for (dm.first = 0; dm.first < a.T; dm.first += most) {
     dm.tokens = static_cast<uint32_t>(a.T - dm.first < most ? a.T - dm.first : most);
     const int64_t blocks = (dm.tokens * per_token + U * kThreads - 1) / (U * kThreads);
-    kv4_read_kernel<TO, U><<<dim3(static_cast<uint32_t>(blocks)), kThreads, 0, s>>>(a, dm);
+    kv4_read_kernel<TO, U, PAST><<<dim3(static_cast<uint32_t>(blocks)), kThreads, 0, s>>>(a, dm);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -94,8 +121,13 @@ hipError_t launch(const Read4Args& a, hipStream_t s) {
   dm.per_token = FastDiv(static_cast<uint32_t>(per_token));
   dm.per_head = FastDiv(a.D / 8);
   dm.keys = static_cast<int>(keys);
-  return a.T * per_token < 256 * 8 * kThreads ? launch_units<TO, 1>(a, dm, s)
-                                              : launch_units<TO, 4>(a, dm, s);
+  if (a.T * per_token < 256 * 8 * kThreads) return launch_units<TO, 1, false>(a, dm, s);
+  // Numbers that fill more than half of the last-level cache (256 MB) are stored
+  // past it: most would be gone before they are read, and what the cache held with
+  // them (50000 rows of 4 heads of 256, three caches in turn: 68 us through it, 40
+  // past it; a plain expansion of bytes of that size 46 and 37).
+  const bool past = a.T * per_token * 8 * static_cast<int64_t>(sizeof(TO)) > int64_t{128} << 20;
+  return past ? launch_units<TO, 4, true>(a, dm, s) : launch_units<TO, 4, false>(a, dm, s);
 }
 
 }  // namespace

@@ -421,6 +421,25 @@ def test_read4_of_every_byte(pq, dev):
     assert torch.equal(out.cpu().nan_to_num(0), want.nan_to_num(0))
 
 
+@pytest.mark.parametrize("dout", [BF16, F32], ids=["bf16", "f32"])
+def test_read4_of_more_than_the_caches_hold(pq, dev, dout):
+    """Outputs past 128 MB are stored another way: the same values, whole and in slices."""
+    T, H, D = 70000, 4, 256
+    cache = filled(pq, dev, 40, 64, H, D, BF16, 3)
+    for s in (cache.k_scale, cache.v_scale):
+        s.copy_(100 + s % 50)
+    slots = torch.randint(-3, 40 * 64 + 3, (T,), generator=torch.Generator().manual_seed(1)).to(dev)
+    k, v = pq.pq1_kv4_read(cache, slots, out_dtype=dout)
+    wide = torch.full((T, H, 2 * D), 7.0, dtype=dout, device=dev)
+    pq.pq1_kv4_read(cache, slots, v_out=wide[:, :, D:])
+    assert torch.equal(wide[:, :, D:], v) and bool((wide[:, :, :D] == 7).all())
+    for at in (0, 30000, T - 1000):
+        some = pq.pq1_kv4_read(cache, slots[at:at + 1000].contiguous(), out_dtype=dout)
+        assert torch.equal(some[0], k[at:at + 1000]) and torch.equal(some[1], v[at:at + 1000])
+    live = (slots >= 0) & (slots < 40 * 64)
+    assert bool((k[~live] == 0).all()) and bool((v[~live] == 0).all())
+
+
 def test_append4_and_read4_past_32_bits(pq, dev):
     """Rows more than 4 GB into the codes."""
     pages, page, H, D = 1 << 14, 64, 16, 512          # 2^24 rows of 256 bytes
