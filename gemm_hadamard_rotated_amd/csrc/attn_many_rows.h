@@ -549,8 +549,8 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
     if constexpr (FOUR) odd_values = __syncthreads_or(odd4) != 0;
     if (odd_values) {
       __syncthreads();
-      put_back_walk<T, TO, F>(a, s, table, h, pt, k0, k1, KT, r0, kTileRows, 64 * kTileWaves, split,
-                      tg.nsplit > 1, part_o);
+      const PartOut to{tg.nsplit > 1, static_cast<int64_t>(split) * a.T * Hq, Hq, part_o, part_ml};
+      put_back_walk<T, TO, F>(a, s, table, h, pt, k0, k1, KT, r0, kTileRows, 64 * kTileWaves, to);
     }
     __syncthreads();  // the next tile of rows takes the buffers
   }

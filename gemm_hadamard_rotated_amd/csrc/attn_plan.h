@@ -21,6 +21,10 @@ struct AttnPlan {
   int chunk = 0;          // keys of a part
   size_t workspace_bytes = 0;
   bool fits = false;      // the grid is launchable
+  // plan_window, few rows: workgroups among which the batch's work is cut evenly;
+  // 0: one takes a (sequence, cache head, row tile) whole
+  int wgs = 0;
+  bool joined = false;    // plan_window: a second launch joins parts
 };
 
 // Which kernel: estimated times, in ns, of a call whose work fills the device.
@@ -117,18 +121,29 @@ inline AttnPlan plan_window(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t
                           (int64_t{sinks} + 63) / 64 * 64;
     return window > 0 && reach < kv ? reach : kv;
   };
-  static_cast<void>(four);
   p.many = prefer_many(B * Hk, rows, walk(kTileRows), D);
   p.tile_rows = p.many ? kTileRows : rows <= 16 ? 16 : 32;
   p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   if (p.row_tiles > most / (B * Hk)) p.row_tiles = most / (B * Hk);
   const int64_t units = B * Hk * p.row_tiles;
   const int64_t keys = walk(p.tile_rows), step = kKeys * kWaves;
-  const int64_t n = parts_of(p.many, units, keys, D);
-  p.chunk = static_cast<int>(((keys + n - 1) / n + step - 1) / step * step);
-  p.nsplit = static_cast<int>((keys + p.chunk - 1) / p.chunk);
-  p.workspace_bytes =
-      p.nsplit > 1 ? static_cast<size_t>(p.nsplit) * T * Hq * (D * 4 + 8) : 0;
+  if (p.many) {
+    const int64_t n = parts_of(true, units, keys, D);
+    p.chunk = static_cast<int>(((keys + n - 1) / n + step - 1) / step * step);
+    p.nsplit = static_cast<int>((keys + p.chunk - 1) / p.chunk);
+    p.joined = p.nsplit > 1;
+    if (p.joined) p.workspace_bytes = static_cast<size_t>(p.nsplit) * T * Hq * (D * 4 + 8);
+    return p;
+  }
+  // Few rows: as many stretches as the device holds at once; whole tiles where they
+  // are short, or so many that they even themselves out.
+  const int per_cu = D == 256 && (!four || p.tile_rows == 32) ? 1 : 2;
+  if (keys * D <= kShort || units >= 2048) return p;
+  const int64_t steps = units * ((keys + step - 1) / step);
+  p.wgs = static_cast<int>(steps < 256 * per_cu ? steps : 256 * per_cu);
+  p.joined = true;
+  p.workspace_bytes = static_cast<size_t>(2 * p.wgs) * p.tile_rows * (D * 4 + 8) +
+                      static_cast<size_t>((T * G / p.tile_rows + B + 1) * Hk) * 8;
   return p;
 }
 

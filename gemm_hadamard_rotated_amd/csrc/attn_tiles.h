@@ -298,19 +298,38 @@ __device__ __forceinline__ float value_at(const Args<F>& a, const T* row, int d)
   }
 }
 
+// Where a workgroup's sums of a row go if they are one part of several: a row of D
+// numbers of `o`, and the maximum and sum in `ml`.
+struct PartOut {  // part after part, the rows of q in each
+  bool partial;
+  int64_t first;  // row 0 of this part
+  int Hq;
+  float* o;
+  float2* ml;
+  __device__ __forceinline__ int64_t at(int, int64_t token, int hq) const {
+    return first + token * Hq + hq;
+  }
+};
+struct SlotOut {  // rows of a tile
+  bool partial;
+  int64_t first;
+  float* o;
+  float2* ml;
+  __device__ __forceinline__ int64_t at(int row, int64_t, int) const { return first + row; }
+};
+
 // Where the values of a tile's edge are not finite, both kernels take them for
 // zero, because times a probability of zero they would be NaN in the rows that
 // do not see them.  Here the rows that do see them add them to their results:
 // rows [r0, r0 + count) of one (sequence, cache head), keys [k0, k1) in tiles
 // of `keys`.  Every thread of the workgroup calls it, after a barrier that
 // follows the stores.
-template <typename T, typename TO, CacheForm F>
+template <typename T, typename TO, CacheForm F, typename Out>
 __device__ __forceinline__ void put_back(const Args<F>& a, const Seq& s, const int32_t* table,
                                          int h, const Parts& pt, int k0, int k1, int keys,
-                                         int64_t r0, int count, int threads, int split,
-                                         bool partial, float* part_o) {
+                                         int64_t r0, int count, int threads,
+                                         const Out& out) {
   const int lane = threadIdx.x & 63;
-  const int Hq = a.Hk * a.G;
   for (int j0 = k0; j0 < k1; j0 += keys) {
     const int j = j0 + lane < k1 ? j0 + lane : k1 - 1;
     const int p = j >> a.page_shift;
@@ -335,8 +354,8 @@ __device__ __forceinline__ void put_back(const Args<F>& a, const Seq& s, const i
         if (j0 + key < lo || j0 + key >= hi) continue;
         const int64_t row = s.q0 + i;
         const int hq = h * a.G + static_cast<int>(r) - i * a.G;
-        if (partial) {
-          part_o[((split * a.T + row) * Hq + hq) * a.D + d] += x;
+        if (out.partial) {
+          out.o[out.at(static_cast<int>(r - r0), row, hq) * a.D + d] += x;
         } else {
           TO* y = static_cast<TO*>(a.out) + row * a.o_ts + hq * a.o_hs + d;
           *y = static_cast<TO>(static_cast<float>(*y) + x);
@@ -347,13 +366,13 @@ __device__ __forceinline__ void put_back(const Args<F>& a, const Seq& s, const i
 }
 
 // The same for places [w0, w1) of the tile's walk.
-template <typename T, typename TO, CacheForm F>
+template <typename T, typename TO, CacheForm F, typename Out>
 __device__ __forceinline__ void put_back_walk(const Args<F>& a, const Seq& s, const int32_t* table,
                                               int h, const Parts& pt, int w0, int w1, int keys,
-                                              int64_t r0, int count, int threads, int split,
-                                              bool partial, float* part_o) {
+                                              int64_t r0, int count, int threads,
+                                              const Out& out) {
   if constexpr (F == kTwoByte) {
-    put_back<T, TO, F>(a, s, table, h, pt, w0, w1, keys, r0, count, threads, split, partial, part_o);
+    put_back<T, TO, F>(a, s, table, h, pt, w0, w1, keys, r0, count, threads, out);
   } else {
     // at most two runs of keys
 #pragma unroll 1
@@ -361,7 +380,7 @@ __device__ __forceinline__ void put_back_walk(const Args<F>& a, const Seq& s, co
       const int last = first < pt.sink_end && pt.sink_end < w1 ? pt.sink_end : w1;
       const int j0 = pt.key_at<F>(first);
       put_back<T, TO, F>(a, s, table, h, pt, j0, j0 + (last - first), keys, r0, count, threads,
-                         split, partial, part_o);
+                         out);
       first = last;
     }
   }

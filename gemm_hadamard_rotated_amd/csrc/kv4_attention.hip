@@ -9,7 +9,7 @@ hipError_t launch_kv4_attention(const AttnPlan& plan, const AttnWindowArgs& a, i
   const hipError_t e = plan.many
                            ? launch_kv4_many_rows(plan, a, dtype, out_dtype, workspace, s)
                            : launch_few_rows<kFourBit>(plan, a, dtype, out_dtype, workspace, s);
-  if (e != hipSuccess || plan.nsplit == 1) return e;
+  if (e != hipSuccess || !plan.joined) return e;
   return join_parts<true>(plan, a, out_dtype, workspace, s);
 }
 

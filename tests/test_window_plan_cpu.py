@@ -28,8 +28,9 @@ int main() {
   while (scanf("%lld %lld %lld %lld %lld %lld %lld %lld %lld %lld", &B, &T, &Hq, &Hk, &D, &mq, &mkv, &w,
                &s, &four) == 10) {
     const pq1::AttnPlan p = pq1::plan_window(B, T, Hq, Hk, D, mq, mkv, w, s, four != 0);
-    printf("%d %d %d %lld %d %d %zu\\n", p.fits, p.many, p.tile_rows,
-           static_cast<long long>(p.row_tiles), p.nsplit, p.chunk, p.workspace_bytes);
+    printf("%d %d %d %lld %d %d %zu %d %d\\n", p.fits, p.many, p.tile_rows,
+           static_cast<long long>(p.row_tiles), p.nsplit, p.chunk, p.workspace_bytes, p.wgs,
+           p.joined);
   }
 }
 """
@@ -81,18 +82,47 @@ def test_parts_cover_what_tiles_walk_over(plans):
                       rng.choice([0, 4, min(log(31), 2 ** 31 - 1)]) if w else 0, rng.randint(0, 1)))
     for size, plan in zip(sizes, plans(sizes)):
         B, T, Hq, Hk, D, mq, mkv, w, s, four = size
-        fits, many, tile_rows, row_tiles, nsplit, chunk, ws = plan
+        fits, many, tile_rows, row_tiles, nsplit, chunk, ws, wgs, joined = plan
         if not fits:
             continue
-        assert nsplit >= 1 and chunk >= 128 and chunk % 128 == 0 and row_tiles >= 1, size
+        assert row_tiles >= 1 and nsplit >= 1, size
+        assert B * Hk * row_tiles * nsplit * (512 if many else 256) < 2 ** 32, size
+        n, kv, G = min(max(mq, 1), T), min(max(mkv, 1), MAX_KEYS), Hq // Hk
+        if not many:
+            # two slots for each stretch, and a note for every row tile there may be
+            assert tile_rows in (16, 32) and nsplit == 1 and wgs <= 512, size
+            tiles = T * G // tile_rows + B + 1
+            assert ws == (2 * wgs * tile_rows * (4 * D + 8) + 8 * tiles * Hk if wgs else 0), size
+            assert joined == (wgs > 0) and (wgs or kv * D <= 98304 or w or B * Hk * row_tiles >= 2048), size
+            continue
+        assert wgs == 0 and joined == (nsplit > 1), size
+        assert chunk >= 128 and chunk % 128 == 0, size
         assert ws == (nsplit * T * Hq * (4 * D + 8) if nsplit > 1 else 0), size
         assert chunk <= MAX_KEYS + 128 and chunk < 2 ** 31, size
-        assert B * Hk * row_tiles * nsplit * (512 if many else 256) < 2 ** 32, size
         # what a stated chunk's tiles walk over fits the parts without stretching them
-        n, kv, G = min(max(mq, 1), T), min(max(mkv, 1), MAX_KEYS), Hq // Hk
         for row0 in (0, tile_rows, (n * G - 1) // tile_rows * tile_rows):
             if row0 < n * G:
                 assert walked(row0, tile_rows, G, n, kv, w, s) <= nsplit * chunk, size
+
+
+def test_notes_of_row_tiles_do_not_meet():
+    """Where the kernels note a tile's pieces: q0 G / ROWS + b on, for sequences that
+    follow one another; and never past the workspace, whatever cu_q holds."""
+    rng = random.Random(1)
+    for _ in range(2000):
+        G, rows = rng.randint(1, 40), rng.choice([16, 32])
+        lens = [rng.choice([0, 1, rng.randint(0, 60)]) for _ in range(rng.randint(1, 12))]
+        q0, last = 0, -1
+        for b, n in enumerate(lens):
+            first, tiles = q0 * G // rows + b, -(-n * G // rows)
+            assert first > last, (G, rows, lens)
+            last = max(last, first + tiles - 1)
+            q0 += n
+        assert last < q0 * G // rows + len(lens) + 1
+        T, B = q0, len(lens)
+        for b in range(B):                       # any two numbers within [0, T]
+            a, z = sorted((rng.randint(0, T), rng.randint(0, T)))
+            assert a * G // rows + b + -(-(z - a) * G // rows) <= T * G // rows + B + 1
 
 
 def attend(lib, fn, q=None, out=None, c=None, table=P(3 * GIB), max_pages=100, cu=P(4 * GIB),  # noqa: F811
