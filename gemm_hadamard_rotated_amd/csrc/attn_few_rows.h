@@ -521,21 +521,29 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void few_rows_kernel
 }
 
 // ---------------------------------------------------------------------------
-// The further forms cut the work of a batch evenly, whatever its lengths: all
-// (sequence, row tile, cache head)s, one after another, are a line of steps of 128
-// keys, and each of as many workgroups as the device holds takes a stretch of the
+// The further forms cut a tile's keys into steps of 128 and those in two ways.
+//
+// Parts: every (sequence, row tile, cache head) in as many parts as the plan says,
+// of equal numbers of steps.
+//
+// Stretches, for batches whose lengths may differ: all tiles' steps, one tile after
+// another (after kStart steps for each one's beginning, which costs as much), are a
+// line, and each of as many workgroups as the device holds takes a stretch of the
 // same length (64 tokens at 200 to 8000 keys, 4-bit, D = 256: 113 us with one
-// workgroup for each, EVEN us cut like this).  Every workgroup finds its stretch by
-// itself, from the sequences' lengths.  Only the first and the last piece of a
-// stretch can be parts of a tile's keys; they go to the stretch's two slots, and
-// the workgroup with a tile's first piece notes for the join who has the others.
+// workgroup for each, 83 in eight parts, 79 with kStart 0, 72 with 2; all at 4000
+// keys: 64, 70, 62 and 63 us).  Every workgroup finds its stretch by itself, from
+// the sequences' lengths.  Only the first and the last piece of a stretch can be
+// parts of a tile's keys; they go to the stretch's two slots, and the workgroup
+// with a tile's first piece notes for the join who has the others.
 // ---------------------------------------------------------------------------
 constexpr int kStep = kKeys * kWaves;
+constexpr int kStart = 2;
 
-struct Stretch {
-  int wgs;             // stretches; 0: a workgroup takes whole tiles
-  int row_tiles;       // of a (sequence, cache head), where wgs is 0
-  FastDiv by_tiles, by_Hk;
+struct Cut {
+  int wgs;        // stretches; 0: parts
+  int row_tiles;  // parts: of a (sequence, cache head), that have workgroups
+  int nsplit;
+  FastDiv by_split, by_tiles, by_Hk;
 };
 
 // Who has a tile's pieces: workgroups first .. first + count - 1.
@@ -544,6 +552,43 @@ struct Pieces {
   int count2;  // 2 count, plus 1 if the first piece begins its stretch
 };
 
+// Where stretches begin: about total w / wgs.  (In fp64, whose division is a tenth of
+// a 64-bit one's code, and the code of a workgroup's only pass is what a short call
+// waits for: any cut will do that all workgroups agree on and that leaves no stretch
+// empty, as the join counts on every one between two others.  With total / wgs at
+// least 1, and for 2^20 workgroups at most, the products are far enough from the
+// integers below them.)
+// The same in all lanes, as the compiler may know.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+  return static_cast<int64_t>(uint64_t{hi} << 32 | lo);
+}
+
+struct Cuts {
+  int wgs;
+  int64_t total;
+  double each;
+  __device__ __forceinline__ int64_t at(int w) const {
+    return w == wgs ? total : uniform(static_cast<int64_t>(each * w));
+  }
+  // The stretch that a step is in.
+  __device__ __forceinline__ int of(int64_t step) const {
+    int w = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<double>(step) / each));
+    w = w < wgs ? w : wgs - 1;
+    if (at(w) > step) --w;
+    if (at(w + 1) <= step) ++w;
+    return w;
+  }
+};
+__device__ __forceinline__ Cuts cuts_of(int wgs, int64_t total) {
+  Cuts c;
+  c.wgs = wgs < total ? wgs : static_cast<int>(total);
+  c.total = total;
+  c.each = static_cast<double>(total) / c.wgs;
+  return c;
+}
+
 template <CacheForm F, int ROWS>
 __device__ __forceinline__ Parts tile_walk(const Args<F>& a, const Seq& s, int64_t r0) {
   return split_keys<F>(a, s, static_cast<int>(r0), ROWS, kMaxKeys, 2);
@@ -551,13 +596,21 @@ __device__ __forceinline__ Parts tile_walk(const Args<F>& a, const Seq& s, int64
 __device__ __forceinline__ int64_t steps_of(const Parts& pt) {
   return pt.end <= 0 ? 1 : (static_cast<int64_t>(pt.end) + kStep - 1) / kStep;
 }
+// Parts of a tile's steps, and where one begins: the first ones have a step more.
+__device__ __forceinline__ uint32_t parts_of_steps(uint32_t nsplit, uint32_t steps) {
+  return nsplit < steps ? nsplit : steps;
+}
+__device__ __forceinline__ uint32_t first_step(uint32_t part, uint32_t parts, uint32_t steps) {
+  const uint32_t each = steps / parts, more = steps - each * parts;
+  return part * each + (part < more ? part : more);
+}
 // Steps of a sequence, all its heads.
 template <CacheForm F, int ROWS>
 __device__ __forceinline__ int64_t steps_of(const Args<F>& a, int64_t b) {
   const Seq s = load_seq(a, b);
   const int64_t rows = static_cast<int64_t>(s.n) * a.G;
   int64_t steps = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += ROWS) steps += steps_of(tile_walk<F, ROWS>(a, s, r0));
+  for (int64_t r0 = 0; r0 < rows; r0 += ROWS) steps += kStart + steps_of(tile_walk<F, ROWS>(a, s, r0));
   return steps * a.Hk;
 }
 // Where the notes of a sequence's row tiles begin: tiles of sequences before it are
@@ -573,70 +626,57 @@ constexpr int kFewPerCu = D == 256 && (F != kFourBit || RB == 2) ? 1 : 2;
 
 template <typename T, typename TO, int D, int RB, bool RUNS, CacheForm F>
 __global__ __launch_bounds__(64 * kWaves, (kFewPerCu<D, RB, F>)) void few_stretch_kernel(
-    Args<F> a, Stretch sg, float* part_o, float2* part_ml, Pieces* pieces) {
+    Args<F> a, Cut sg, float* part_o, float2* part_ml, Pieces* pieces) {
   constexpr int ROWS = 16 * RB;
-  __shared__ int64_t wave_steps[kWaves], found_at;
-  __shared__ int found_b;
   const int w = blockIdx.x;
-  int64_t begin = 0, end = 0, total = 0, wgs = 0, at = 0;
+  int64_t begin = 0, end = 0, at = 0;
   int64_t pos = 0;  // of the present tile's first step
+  Cuts cuts{0, 0, 0};
   int b;
   int h = 0;
   int64_t r0 = 0;
+  uint32_t split = 0;
   if (sg.wgs == 0) {
-    const uint32_t id1 = sg.by_tiles.div(blockIdx.x), rt = blockIdx.x - id1 * sg.by_tiles.d;
+    // first parts first: a part's number must not decide the XCD
+    split = sg.by_split.div(blockIdx.x);
+    const uint32_t id0 = blockIdx.x - split * sg.by_split.d;
+    const uint32_t id1 = sg.by_tiles.div(id0), rt = id0 - id1 * sg.by_tiles.d;
     b = sg.by_Hk.div(id1);
     h = id1 - b * sg.by_Hk.d;
     r0 = static_cast<int64_t>(rt) * ROWS;
   } else {
-    // steps of each thread's sequences, summed up over the threads before it
-    const int64_t each = (a.B + 64 * kWaves - 1) / (64 * kWaves);
-    const int64_t b0 = threadIdx.x * each, b1 = b0 + each < a.B ? b0 + each : a.B;
+    // Every wave for itself: steps of a lane's sequences, summed up over the lanes.
+    const int each = static_cast<int>((a.B + 63) / 64), lane = threadIdx.x & 63;
+    const int b0 = lane * each, b1 = b0 + each < a.B ? b0 + each : static_cast<int>(a.B);
     int64_t mine = 0;
-    for (int64_t i = b0; i < b1; ++i) mine += steps_of<F, ROWS>(a, i);
+#pragma unroll 1
+    for (int i = b0; i < b1; ++i) mine += steps_of<F, ROWS>(a, i);
     int64_t sum = mine;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
+#pragma unroll 1
     for (int m = 1; m < 64; m <<= 1) {
       const int64_t x = __shfl_up(sum, m);
       if (lane >= m) sum += x;
     }
-    if (lane == 63) wave_steps[wave] = sum;
-    if (threadIdx.x == 0) found_b = 0, found_at = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-      if (i < wave) sum += wave_steps[i];
-      total += wave_steps[i];
-    }
-    // no stretch without a step: the join counts on every one between two others
-    wgs = sg.wgs < total ? sg.wgs : total;
-    if (w < wgs) {
-      begin = total * w / wgs;
-      end = total * (w + 1) / wgs;
-    }
-    int64_t before = sum - mine;
-    if (begin < end && before <= begin && begin < sum) {  // this thread's sequences have the first step
-      int64_t i = b0;
-      for (; i + 1 < b1; ++i) {
-        const int64_t steps = steps_of<F, ROWS>(a, i);
-        if (before + steps > begin) break;
-        before += steps;
-      }
-      found_b = static_cast<int>(i);
-      found_at = before;
-    }
-    __syncthreads();
-    b = __builtin_amdgcn_readfirstlane(found_b);
-    if (begin < end) {
-      // the tile and head in it that the first step is of
-      pos = found_at;
-      const Seq s = load_seq(a, b);
+    cuts = cuts_of(sg.wgs, uniform(__shfl(sum, 63)));
+    if (w < cuts.wgs) {
+      begin = cuts.at(w);
+      end = cuts.at(w + 1);
+      // the sequence, row tile and head that the first step is of
+      const uint64_t past = __ballot(sum > begin);
+      const int who = __builtin_ctzll(past);
+      pos = uniform(__shfl(sum - mine, who));
+      b = __builtin_amdgcn_readfirstlane(who * each);
+#pragma unroll 1
       for (;; r0 += ROWS) {
-        const int64_t steps = steps_of(tile_walk<F, ROWS>(a, s, r0));
+        const Seq s = load_seq(a, b);
+        if (r0 >= static_cast<int64_t>(s.n) * a.G) {
+          ++b;
+          r0 = -ROWS;
+          continue;
+        }
+        const int64_t steps = kStart + steps_of(tile_walk<F, ROWS>(a, s, r0));
         if (pos + steps * a.Hk > begin) {
-          h = static_cast<int>((begin - pos) / steps);
-          pos += h * steps;
+          while (pos + steps <= begin) pos += steps, ++h;
           break;
         }
         pos += steps * a.Hk;
@@ -655,30 +695,39 @@ __global__ __launch_bounds__(64 * kWaves, (kFewPerCu<D, RB, F>)) void few_stretc
       continue;
     }
     const Parts pt = tile_walk<F, ROWS>(a, s, r0);
-    int k0 = 0, k1 = pt.end;
-    SlotOut out{false, 0, part_o, part_ml};
+    int k0, k1;
+    SlotOut out{false, sg.wgs > 0, 0, a.Hk * a.G, part_o, part_ml};
     const int64_t r = r0;
     const int head = h;
     if (sg.wgs == 0) {
       r0 += static_cast<int64_t>(sg.row_tiles) * ROWS;
+      const uint32_t steps = static_cast<uint32_t>(steps_of(pt));
+      const uint32_t parts = parts_of_steps(sg.nsplit, steps);
+      if (split >= parts) continue;
+      k0 = static_cast<int>(first_step(split, parts, steps)) * kStep;
+      k1 = split + 1 < parts ? static_cast<int>(first_step(split + 1, parts, steps)) * kStep : pt.end;
+      out.partial = parts > 1;
+      out.first = static_cast<int64_t>(split) * a.T * out.Hq;
     } else {
-      const int64_t steps = steps_of(pt), off = at - pos;
+      // places [off, off + n) of the tile's steps, of which the first kStart have no keys
+      const int64_t steps = kStart + steps_of(pt), off = at - pos;
       const int64_t n = steps - off < end - at ? steps - off : end - at;
-      k0 = static_cast<int>(off * kStep);
-      k1 = pt.end - k0 < n * kStep ? pt.end : k0 + static_cast<int>(n * kStep);
-      out.partial = n < steps;
+      const int64_t first = off > kStart ? off - kStart : 0, last = off + n - kStart;
+      k0 = static_cast<int>(first * kStep);
+      k1 = off + n < steps ? static_cast<int>(last * kStep) : pt.end;
+      out.partial = first > 0 || off + n < steps;
       out.first = (int64_t{2} * w + (at == begin ? 0 : 1)) * ROWS;
-      if (off == 0 && threadIdx.x == 0) {
-        // the last step's workgroup is the last whose stretch begins at or before it
-        const int64_t last = out.partial ? (wgs * (pos + steps) - 1) / total : w;
+      if (first == 0 && last > 0 && threadIdx.x == 0) {
+        const int has_end = out.partial ? cuts.of(pos + steps - 1) : w;
         pieces[(first_tile<ROWS>(a, s, b) + r / ROWS) * a.Hk + head] =
-            {w, 2 * static_cast<int>(last - w + 1) + (at == begin)};
+            {w, 2 * (has_end - w + 1) + (at == begin)};
       }
       at += n;
       if (off + n == steps) {
         pos += steps;
         if (++h == a.Hk) h = 0, r0 += ROWS;
       }
+      if (last <= 0) continue;  // the beginning alone: the next workgroup's
     }
     few_rows_part<T, TO, D, RB, RUNS, F>(a, s, a.table + static_cast<int64_t>(b) * a.max_pages,
                                          head, static_cast<int>(rows), r, pt, k0, k1, out);
@@ -791,9 +840,9 @@ __global__ __launch_bounds__(256) void join_kernel(Args<SINKS ? kTwoByteSinks : 
   }
 }
 
-// The same for rows whose parts are the pieces of stretches.
-template <typename TO, int D, int WPR, int ROWS>
-__global__ __launch_bounds__(256) void join_pieces_kernel(AttnWindowArgs a, int tokens,
+// The same for the rows of few_stretch_kernel (ROWS in a tile).
+template <typename TO, int D, int WPR, int ROWS, CacheForm F>
+__global__ __launch_bounds__(256) void join_pieces_kernel(Args<F> a, Cut cut, int tokens,
                                                           const float* part_o,
                                                           const float2* part_ml,
                                                           const Pieces* pieces) {
@@ -809,8 +858,15 @@ __global__ __launch_bounds__(256) void join_pieces_kernel(AttnWindowArgs a, int 
   const int h = static_cast<int>(a.by_G.div(hq)), hq_in = hq - h * a.G;
   for (int i = id - b * tokens; i < s.n; i += tokens) {
     const int64_t r = static_cast<int64_t>(i) * a.G + hq_in, tile = r / ROWS;
-    const Pieces p = pieces[(first_tile<ROWS>(a, s, b) + tile) * a.Hk + h];
-    const int count = p.count2 >> 1;
+    Pieces p{0, 0};
+    int count;
+    if (cut.wgs == 0) {
+      const Parts pt = tile_walk<F, ROWS>(a, s, tile * ROWS);
+      count = static_cast<int>(parts_of_steps(cut.nsplit, static_cast<uint32_t>(steps_of(pt))));
+    } else {
+      p = pieces[(first_tile<ROWS>(a, s, b) + tile) * a.Hk + h];
+      count = p.count2 >> 1;
+    }
     if (count <= 1) continue;  // the workgroup that had it all wrote the result
     int lo, hi;
     visible(a, s, i, &lo, &hi);
@@ -818,7 +874,7 @@ __global__ __launch_bounds__(256) void join_pieces_kernel(AttnWindowArgs a, int 
     join_row<TO, D, WPR>(
         a, part_o, part_ml, count, hi > lo, s.q0 + i, hq, [&](int part) -> int64_t {
           const int slot = 2 * (p.first + part) + (part == 0 && !(p.count2 & 1));
-          return int64_t{slot} * ROWS + row;
+          return cut.wgs == 0 ? (part * a.T + s.q0 + i) * Hq + hq : int64_t{slot} * ROWS + row;
         });
   }
 }
@@ -827,6 +883,19 @@ FewGrid grid_of(const AttnPlan& plan, const AttnArgs& a) {
   return {static_cast<int>(plan.row_tiles), plan.nsplit, plan.chunk,
           FastDiv(static_cast<uint32_t>(plan.row_tiles)),
           FastDiv(static_cast<uint32_t>(plan.nsplit)), FastDiv(static_cast<uint32_t>(a.Hk))};
+}
+
+Cut cut_of(const AttnPlan& plan, const AttnArgs& a) {
+  return {plan.wgs,
+          static_cast<int>(plan.row_tiles),
+          plan.nsplit,
+          FastDiv(static_cast<uint32_t>(a.B * a.Hk * plan.row_tiles)),
+          FastDiv(static_cast<uint32_t>(plan.row_tiles)),
+          FastDiv(static_cast<uint32_t>(a.Hk))};
+}
+// Rows of a cut's partial sums.
+int64_t cut_rows(const AttnPlan& plan, const AttnArgs& a) {
+  return plan.wgs > 0 ? int64_t{2} * plan.wgs * plan.tile_rows : plan.nsplit * a.T * a.Hk * a.G;
 }
 
 template <typename T, typename TO, int D, int RB, CacheForm F>
@@ -844,19 +913,17 @@ hipError_t launch_few(const AttnPlan& plan, const Args<F>& a, void* workspace, h
     else
       few_rows_kernel<T, TO, D, RB, false><<<grid, 64 * kWaves, 0, s>>>(a, fg, part_o, part_ml);
   } else {
-    const Stretch sg{plan.wgs, static_cast<int>(plan.row_tiles),
-                     FastDiv(static_cast<uint32_t>(plan.row_tiles)),
-                     FastDiv(static_cast<uint32_t>(a.Hk))};
-    const int64_t rows = int64_t{2} * plan.wgs * plan.tile_rows;
-    float2* part_ml = reinterpret_cast<float2*>(part_o + rows * D);
-    Pieces* pieces = reinterpret_cast<Pieces*>(part_ml + rows);
-    const dim3 grid(static_cast<uint32_t>(plan.wgs > 0 ? plan.wgs : a.B * a.Hk * plan.row_tiles));
+    const Cut cut = cut_of(plan, a);
+    float2* part_ml = reinterpret_cast<float2*>(part_o + cut_rows(plan, a) * D);
+    Pieces* pieces = reinterpret_cast<Pieces*>(part_ml + cut_rows(plan, a));
+    const dim3 grid(static_cast<uint32_t>(
+        plan.wgs > 0 ? plan.wgs : a.B * a.Hk * plan.row_tiles * plan.nsplit));
     if (runs)
       few_stretch_kernel<T, TO, D, RB, true, F>
-          <<<grid, 64 * kWaves, 0, s>>>(a, sg, part_o, part_ml, pieces);
+          <<<grid, 64 * kWaves, 0, s>>>(a, cut, part_o, part_ml, pieces);
     else
       few_stretch_kernel<T, TO, D, RB, false, F>
-          <<<grid, 64 * kWaves, 0, s>>>(a, sg, part_o, part_ml, pieces);
+          <<<grid, 64 * kWaves, 0, s>>>(a, cut, part_o, part_ml, pieces);
   }
   return hipGetLastError();
 }
@@ -865,20 +932,21 @@ template <typename TO, int D, int WPR>
 hipError_t launch_pieces(const AttnPlan& plan, const AttnWindowArgs& a, void* workspace,
                          hipStream_t s) {
   const float* part_o = static_cast<const float*>(workspace);
-  const int64_t rows = int64_t{2} * plan.wgs * plan.tile_rows;
-  const float2* part_ml = reinterpret_cast<const float2*>(part_o + rows * D);
-  const Pieces* pieces = reinterpret_cast<const Pieces*>(part_ml + rows);
+  const float2* part_ml = reinterpret_cast<const float2*>(part_o + cut_rows(plan, a) * D);
+  const Pieces* pieces = reinterpret_cast<const Pieces*>(part_ml + cut_rows(plan, a));
   constexpr int RPW = 4 / WPR;
   const int64_t groups = (a.Hk * a.G + RPW - 1) / RPW;
   const int64_t most = ((int64_t{1} << 24) - 1) / (a.B * groups);  // below 2^32 threads
   const int64_t tokens = plan.tokens < most ? plan.tokens : most;
   const dim3 grid(static_cast<uint32_t>(a.B * tokens * groups));
+  const Cut cut = cut_of(plan, a);
+  const int n = static_cast<int>(tokens);
   if (plan.tile_rows == 16)
-    join_pieces_kernel<TO, D, WPR, 16><<<grid, 256, 0, s>>>(a, static_cast<int>(tokens), part_o,
-                                                            part_ml, pieces);
+    join_pieces_kernel<TO, D, WPR, 16, kTwoByteSinks>
+        <<<grid, 256, 0, s>>>(a, cut, n, part_o, part_ml, pieces);
   else
-    join_pieces_kernel<TO, D, WPR, 32><<<grid, 256, 0, s>>>(a, static_cast<int>(tokens), part_o,
-                                                            part_ml, pieces);
+    join_pieces_kernel<TO, D, WPR, 32, kTwoByteSinks>
+        <<<grid, 256, 0, s>>>(a, cut, n, part_o, part_ml, pieces);
   return hipGetLastError();
 }
 
@@ -906,7 +974,7 @@ hipError_t launch_join(const AttnPlan& plan, const JoinArgs<SINKS>& a, void* wor
   if constexpr (SINKS) {
     // as below, by the pieces of a tile where there are few
     if (!plan.many)
-      return plan.wgs > 8 * a.B * a.Hk * plan.row_tiles
+      return plan.nsplit > 8 || plan.wgs > 8 * a.B * a.Hk * plan.row_tiles
                  ? launch_pieces<TO, D, 4>(plan, a, workspace, s)
                  : launch_pieces<TO, D, 1>(plan, a, workspace, s);
   }

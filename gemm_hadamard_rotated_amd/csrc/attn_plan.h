@@ -22,7 +22,7 @@ struct AttnPlan {
   size_t workspace_bytes = 0;
   bool fits = false;      // the grid is launchable
   // plan_window, few rows: workgroups among which the batch's work is cut evenly;
-  // 0: one takes a (sequence, cache head, row tile) whole
+  // 0: nsplit parts of every (sequence, cache head, row tile)
   int wgs = 0;
   bool joined = false;    // plan_window: a second launch joins parts
 };
@@ -47,6 +47,11 @@ inline bool prefer_many(int64_t units, int64_t rows, int64_t keys, int D) {
 // another: 300 keys 10.9 us in one part and 14.7 in several, 700 keys 17.4 and
 // 14.6; at D = 128 700 keys 10.8 and 14.5, 1500 keys 16.7 and 14.7.
 constexpr int64_t kShort = 98304;
+// plan_window: with parts as short as that a batch of different lengths is not
+// worth cutting evenly: finding a stretch costs 2 us and more (4-bit, D = 256, in
+// parts and in stretches: one sequence of 700 keys 14.1 and 14.9 us, of 131070 42
+// and 45; 16 sequences of 4000 22 and 24; 200 of 1000 54 and 63).
+constexpr int64_t kPart = 262144;
 
 // Parts of that many keys for so many (sequence, cache head, row tile)s.
 inline int64_t parts_of(bool many, int64_t units, int64_t keys, int D) {
@@ -135,13 +140,22 @@ inline AttnPlan plan_window(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t
     if (p.joined) p.workspace_bytes = static_cast<size_t>(p.nsplit) * T * Hq * (D * 4 + 8);
     return p;
   }
-  // Few rows: as many stretches as the device holds at once; whole tiles where they
-  // are short, or so many that they even themselves out.
+  // Few rows: whole tiles where keys are few, where a window keeps the lengths alike
+  // (48 sequences, window of 1024, 8 cache heads, D = 128, two-byte: 46 us, 54 in
+  // stretches) and where tiles are many; parts for one sequence or where they are
+  // short; else stretches, as many as the device holds at once.
   const int per_cu = D == 256 && (!four || p.tile_rows == 32) ? 1 : 2;
-  if (keys * D <= kShort || units >= 2048) return p;
-  const int64_t steps = units * ((keys + step - 1) / step);
-  p.wgs = static_cast<int>(steps < 256 * per_cu ? steps : 256 * per_cu);
+  const int64_t slots = 256 * per_cu, steps = (keys + step - 1) / step;
+  const int64_t n = (slots + units - 1) / units;
+  if (keys * D <= kShort || units >= (window > 0 ? 256 : 4 * slots)) return p;
   p.joined = true;
+  if (B == 1 || keys * D <= n * kPart) {
+    p.nsplit = static_cast<int>(n < steps ? n : steps);
+    p.joined = p.nsplit > 1;
+    if (p.joined) p.workspace_bytes = static_cast<size_t>(p.nsplit) * T * Hq * (D * 4 + 8);
+    return p;
+  }
+  p.wgs = static_cast<int>(units * steps < slots ? units * steps : slots);
   p.workspace_bytes = static_cast<size_t>(2 * p.wgs) * p.tile_rows * (D * 4 + 8) +
                       static_cast<size_t>((T * G / p.tile_rows + B + 1) * Hk) * 8;
   return p;

@@ -310,12 +310,16 @@ struct PartOut {  // part after part, the rows of q in each
     return first + token * Hq + hq;
   }
 };
-struct SlotOut {  // rows of a tile
+struct SlotOut {  // the same, or the rows of a tile in a slot
   bool partial;
+  bool slot;
   int64_t first;
+  int Hq;
   float* o;
   float2* ml;
-  __device__ __forceinline__ int64_t at(int row, int64_t, int) const { return first + row; }
+  __device__ __forceinline__ int64_t at(int row, int64_t token, int hq) const {
+    return first + (slot ? row : token * Hq + hq);
+  }
 };
 
 // Where the values of a tile's edge are not finite, both kernels take them for

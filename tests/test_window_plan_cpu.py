@@ -89,11 +89,13 @@ def test_parts_cover_what_tiles_walk_over(plans):
         assert B * Hk * row_tiles * nsplit * (512 if many else 256) < 2 ** 32, size
         n, kv, G = min(max(mq, 1), T), min(max(mkv, 1), MAX_KEYS), Hq // Hk
         if not many:
-            # two slots for each stretch, and a note for every row tile there may be
-            assert tile_rows in (16, 32) and nsplit == 1 and wgs <= 512, size
+            # the rows of each part; or two slots for each stretch, and a note for every
+            # row tile there may be
+            assert tile_rows in (16, 32) and wgs <= 768 and (nsplit == 1 or wgs == 0), size
             tiles = T * G // tile_rows + B + 1
-            assert ws == (2 * wgs * tile_rows * (4 * D + 8) + 8 * tiles * Hk if wgs else 0), size
-            assert joined == (wgs > 0) and (wgs or kv * D <= 98304 or w or B * Hk * row_tiles >= 2048), size
+            parts = nsplit * T * Hq * (4 * D + 8) if nsplit > 1 else 0
+            assert ws == (2 * wgs * tile_rows * (4 * D + 8) + 8 * tiles * Hk if wgs else parts), size
+            assert joined == (wgs > 0 or nsplit > 1), size
             continue
         assert wgs == 0 and joined == (nsplit > 1), size
         assert chunk >= 128 and chunk % 128 == 0, size
