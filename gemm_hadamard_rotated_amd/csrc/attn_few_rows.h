@@ -155,7 +155,9 @@ __device__ __forceinline__ void few_rows_part(const Args<F>& a, const Seq& s, co
         const_cast<uint8_t*>(static_cast<const uint8_t*>(array) + t.row[e] * n), 0, t.keys[e] * n,
         0x00020000);
   };
-  // Keys past the last read as zeros (RUNS) or as some row of the cache.
+  // Keys past the last read as zeros (RUNS) or as some row of the cache.  (Pieces by the
+  // scalar offset: what comes of adding them up may order the loads otherwise than
+  // the products want them, 236 us for 232 in a decode of 64 at D = 256.)
   auto load_k = [&](const TileAt& t, int j0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -196,7 +198,7 @@ __device__ __forceinline__ void few_rows_part(const Args<F>& a, const Seq& s, co
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
           kr[e][d] =
-              __builtin_amdgcn_raw_buffer_load_b128(run, (col * D + 8 * g + 32 * d) * 2, 0, 0);
+              __builtin_amdgcn_raw_buffer_load_b128(run, (col * D + 8 * g) * 2, 64 * d, 0);
       } else {
         const T* src = static_cast<const T*>(a.k_cache) + row_of(t, j0, 16 * e + col) * D + 8 * g;
 #pragma unroll
