@@ -31,6 +31,8 @@
 // prompts 386 -> 377).
 #pragma once
 
+#include <type_traits>
+
 #include "attn_tiles.h"
 
 namespace pq1 {
@@ -110,7 +112,13 @@ constexpr int kTileWaves = kTileRows / 32;
 
 // Four-bit caches (F = kFourBit): a thread reads 8 or 16 codes of one K and one V row
 // into registers, a tile before they are wanted, and writes them to LDS as numbers of
-// T, where the products find them as they find copied ones.
+// T, where the products find them as they find copied ones.  Of a SIMD's two waves one
+// does so before its products and one after them, so that while one converts the
+// other keeps the matrix pipe (2048 tokens after 6144, D = 256: 405 us with both
+// before, 396 both after, 366 so; 8 prompts of 300 to 2000 tokens 942, 910 and 841).
+// With the second product taken more than once, for an fp32 result, both do so before
+// (1000 tokens after 4000, bf16: 300 us at D = 256 and 163 at 128; one of them after
+// 336 and 174).
 template <typename T, typename TO, int D, bool WIDE, CacheForm F>
 __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, TileGrid tg,
                                                                     float* part_o,
@@ -174,7 +182,8 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
 
     // Pages of keys first .. end - 1 are in LDS: the number, -1 for no page of
     // the cache; or, where K and V take less than 4 GB each, the byte at which
-    // the page's rows of this head begin, one more than page 0's for none.
+    // the page's rows of this head begin, one more than page 0's for none (4-bit
+    // caches: twice the number of their first row).
     // Keys past the last take its page, so that every address lies in the
     // cache.  A lane looks up the rows that it copies, a tile ahead.
     // With sinks `first` and `end` are places of the walk; page_lds[0] is page
@@ -253,17 +262,22 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
     auto fetch4 = [&](int w0) {
       const int w = up_to_end(w0 + static_cast<int>(threadIdx.x) / PER_ROW);
       const int piece = threadIdx.x % PER_ROW;
-      const int page = page_at(w);
-      const int64_t row = ((static_cast<int64_t>(page < 0 ? 0 : page) * a.Hk + h) << a.page_shift) +
-                          (pt.key_at<F>(w) & page_mask);
-      const int64_t at = row * (D / 2) + piece * (CODES / 2);
-      const int64_t sat = row * (D / kGroup4) + piece * CODES / kGroup4;
-      const uint8_t* k = static_cast<const uint8_t*>(a.k_cache) + at;
-      const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + at;
+      const int page = page_at(w), in_page = pt.key_at<F>(w) & page_mask;
+      using Offset = std::conditional_t<WIDE, int64_t, uint32_t>;
+      Offset row;
+      if constexpr (WIDE)
+        row = ((static_cast<int64_t>(page < 0 ? 0 : page) * a.Hk + h) << a.page_shift) + in_page;
+      else
+        row = (static_cast<uint32_t>(page) >> 1) + in_page;
+      const Offset at = row * (D / 2) + piece * (CODES / 2);
+      const Offset sat = row * (D / kGroup4) + piece * CODES / kGroup4;
+      using Codes = __attribute__((ext_vector_type(WORDS))) uint32_t;
+      const Codes k = *reinterpret_cast<const Codes*>(static_cast<const uint8_t*>(a.k_cache) + at);
+      const Codes v = *reinterpret_cast<const Codes*>(static_cast<const uint8_t*>(a.v_cache) + at);
 #pragma unroll
       for (int n = 0; n < WORDS; ++n) {
-        kc[n] = reinterpret_cast<const uint32_t*>(k)[n];
-        vc[n] = reinterpret_cast<const uint32_t*>(v)[n];
+        kc[n] = k[n];
+        vc[n] = v[n];
       }
       if constexpr (FOUR) {
         kscale = a.k_scale[sat];
@@ -459,7 +473,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
           page_lds[p - p0] = bad ? -1 : page;
         else
           page_lds[p - p0] = (((static_cast<uint32_t>(bad ? 0 : page) * a.Hk + h) << a.page_shift) *
-                              ROWB) | bad;
+                              (FOUR ? 2 : ROWB)) | bad;
         lost |= bad;
       }
       const bool any_gone = __syncthreads_or(lost);
@@ -473,11 +487,16 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
 #pragma unroll 1
         for (int w0 = first; w0 < end; w0 += KT) {
           const int then = now == 0 ? TILE : 0;
-          if (w0 + KT < end) widen4(w0 + KT, lost_of(w0 + KT), k_lds + then, v_lds + then);
-          fetch4(w0 + 2 * KT);
+          auto advance = [&] {
+            if (w0 + KT < end) widen4(w0 + KT, lost_of(w0 + KT), k_lds + then, v_lds + then);
+            fetch4(w0 + 2 * KT);
+          };
+          const bool early = NP > 1 || wave < kTileWaves / 2;
           F16 sc[EB];
+          if (early) advance();
           scores(k_lds + now, sc);
           products(v_lds + now, pt.key_at<F>(w0), lost_of(w0), sc);
+          if (!early) advance();
           __syncthreads();
           now = then;
         }
@@ -563,17 +582,14 @@ hipError_t launch_tiles(const AttnPlan& plan, const Args<F>& a, void* workspace,
   float2* part_ml =
       reinterpret_cast<float2*>(part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
   const dim3 grid(static_cast<uint32_t>(a.B * a.Hk * plan.row_tiles * plan.nsplit));
-  if constexpr (F == kFourBit) {
+  // 32-bit offsets into K and V where they reach (D = 64 of the above: 193 us
+  // with 64-bit ones, 186 with these)
+  const uint64_t cache_rows = static_cast<uint64_t>(a.pages) * a.Hk << a.page_shift;
+  const bool wide = (cache_rows * (F == kFourBit ? D / 2 : 2 * D)) >> 32 != 0;
+  if (wide)
     many_rows_kernel<T, TO, D, true, F><<<grid, 64 * kTileWaves, 0, s>>>(a, tg, part_o, part_ml);
-  } else {
-    // 32-bit offsets into K and V where they reach (D = 64 of the above: 193 us
-    // with 64-bit ones, 186 with these)
-    const bool wide = ((static_cast<uint64_t>(a.pages) * a.Hk << a.page_shift) * 2 * D) >> 32 != 0;
-    if (wide)
-      many_rows_kernel<T, TO, D, true, F><<<grid, 64 * kTileWaves, 0, s>>>(a, tg, part_o, part_ml);
-    else
-      many_rows_kernel<T, TO, D, false, F><<<grid, 64 * kTileWaves, 0, s>>>(a, tg, part_o, part_ml);
-  }
+  else
+    many_rows_kernel<T, TO, D, false, F><<<grid, 64 * kTileWaves, 0, s>>>(a, tg, part_o, part_ml);
   return hipGetLastError();
 }
 
