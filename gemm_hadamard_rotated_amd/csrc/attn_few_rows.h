@@ -831,8 +831,8 @@ __global__ __launch_bounds__(256) void join_kernel(Args<SINKS ? kTwoByteSinks : 
   for (int i = id - b * tokens; i < s.n; i += tokens) {
     const int r = i * a.G + hq_in;
     // a tile's rows are a power of two
-    const Parts pt = split_keys<SINKS ? kTwoByteSinks : kTwoByte>(a, s, r & -tile_rows, tile_rows,
-                                                                  fg.chunk, fg.nsplit);
+    const Parts pt = split_keys<SINKS ? kTwoByteSinks : kTwoByte, kTileKeys<D>>(
+        a, s, r & -tile_rows, tile_rows, fg.chunk, fg.nsplit);
     const int count = pt.count();
     int lo, hi;
     visible(a, s, i, &lo, &hi);

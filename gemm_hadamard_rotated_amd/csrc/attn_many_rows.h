@@ -124,7 +124,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
                                                                     float* part_o,
                                                                     float2* part_ml) {
   constexpr int NP = kParts<T, TO>;
-  constexpr int KT = D == 256 ? 32 : 64;        // keys of a tile
+  constexpr int KT = kTileKeys<D>;
   constexpr int ROWB = 2 * D;                   // bytes of a cache row
   constexpr int TILE = KT * ROWB;
   constexpr int PIECES = D / 8;                 // 16-byte pieces of a row
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
 
   for (int64_t r0 = static_cast<int64_t>(rt) * kTileRows; r0 < rows;
        r0 += static_cast<int64_t>(tg.row_tiles) * kTileRows) {
-    const Parts pt = split_keys<F>(a, s, static_cast<int>(r0), kTileRows, tg.chunk, tg.nsplit);
+    const Parts pt = split_keys<F, KT>(a, s, static_cast<int>(r0), kTileRows, tg.chunk, tg.nsplit);
     if (split > 0 && split >= pt.count()) continue;
     const int k0 = pt.start + split * pt.chunk;
     const int k1 = pt.end - k0 < pt.chunk ? pt.end : k0 + pt.chunk;

@@ -10,6 +10,8 @@ namespace pq1 {
 constexpr int kTileRows = 256;  // rows of a many-rows tile
 constexpr int kKeys = 32;       // keys of a tile of the few-rows kernel
 constexpr int kWaves = 4;       // waves of its workgroup
+template <int D>
+constexpr int kTileKeys = D == 256 ? 32 : 64;  // keys of a tile of the many-rows kernel
 constexpr int kMaxKeys = 0x7fff0000;  // of a sequence: key numbers plus a tile stay in 31 bits
 
 struct AttnPlan {
@@ -122,8 +124,9 @@ inline AttnPlan plan_window(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t
     // the window of its first row, a key more for each token after that, the
     // rounding of the start, and the first keys, rounded up
     const int64_t tokens = (tile_rows + G - 1) / G + 1;
-    const int64_t reach = int64_t{window} + (tokens < p.tokens ? tokens : p.tokens) - 1 + 63 +
-                          (int64_t{sinks} + 63) / 64 * 64;
+    const int64_t tile = tile_rows < kTileRows ? kKeys : D == 256 ? kTileKeys<256> : kTileKeys<64>;
+    const int64_t reach = int64_t{window} + (tokens < p.tokens ? tokens : p.tokens) - 1 + tile - 1 +
+                          (int64_t{sinks} + tile - 1) / tile * tile;
     return window > 0 && reach < kv ? reach : kv;
   };
   p.many = prefer_many(B * Hk, rows, walk(kTileRows), D);

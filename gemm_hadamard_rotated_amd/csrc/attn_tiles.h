@@ -54,7 +54,7 @@ __device__ __forceinline__ void visible(const AttnArgs& a, const Seq& s, int i, 
 // and key w + jump past it.  Both are multiples of 64, so that a tile of keys has
 // no jump inside.  Elsewhere places are keys.
 struct Parts {
-  int start;  // rounded down to a multiple of 32 (64 with sinks)
+  int start;  // rounded down to a multiple of 32
   int end;
   int lo, hi;  // keys that some row sees (and the first ones)
   int lo_max, hi_min;  // keys in [lo_max, hi_min) are seen by every row
@@ -70,7 +70,8 @@ struct Parts {
   }
 };
 
-template <CacheForm F>
+// (With sinks both pieces of the walk are whole key tiles, of KEYS.)
+template <CacheForm F, int KEYS = kKeys>
 __device__ __forceinline__ Parts split_keys(const Args<F>& a, const Seq& s, int r0, int rows,
                                             int chunk, int nsplit) {
   const int last = s.n * a.G - 1;
@@ -84,9 +85,9 @@ __device__ __forceinline__ Parts split_keys(const Args<F>& a, const Seq& s, int 
   p.lo = lo0;
   p.hi = hi1;
   if constexpr (F != kTwoByte) {
-    const int first = lo0 & ~63;  // of the window
+    const int first = lo0 & ~(KEYS - 1);  // of the window
     const int sinks = a.sinks < kMaxKeys ? a.sinks : kMaxKeys;
-    p.sink_end = (sinks + 63) & ~63;
+    p.sink_end = (sinks + KEYS - 1) & ~(KEYS - 1);
     p.jump = first > p.sink_end ? first - p.sink_end : 0;
     p.start = 0;
     p.end = hi1 - p.jump;

@@ -58,13 +58,13 @@ def plans(tmp_path_factory):
     return run
 
 
-def walked(row0, rows, G, n, kv, w, s):
+def walked(row0, rows, G, n, kv, w, s, tile):
     """Keys that a tile of these rows walks over, as the kernels do: the first keys
-    rounded up to 64, then the window from its start rounded down to 64."""
+    rounded up to key tiles, then the window from its start rounded down to them."""
     i0, i1 = row0 // G, min(row0 + rows - 1, n * G - 1) // G
     end = max(0, kv - (n - 1 - i1))
     lo = max(0, kv - (n - 1 - i0) - w) if w else 0
-    first, sink_end = lo // 64 * 64, -(-s // 64) * 64
+    first, sink_end = lo // tile * tile, -(-s // tile) * tile
     return end - max(0, first - sink_end)
 
 
@@ -104,7 +104,7 @@ def test_parts_cover_what_tiles_walk_over(plans):
         # what a stated chunk's tiles walk over fits the parts without stretching them
         for row0 in (0, tile_rows, (n * G - 1) // tile_rows * tile_rows):
             if row0 < n * G:
-                assert walked(row0, tile_rows, G, n, kv, w, s) <= nsplit * chunk, size
+                assert walked(row0, tile_rows, G, n, kv, w, s, 32 if D == 256 else 64) <= nsplit * chunk, size
 
 
 def test_notes_of_row_tiles_do_not_meet():
