@@ -36,9 +36,15 @@ struct AttnPlan {
 // cache heads, few rows against many: 64 sequences of 1000 keys, 24 rows 46 and
 // 82 us, 72 rows 120 and 87; one sequence of 8000 keys, 48 rows 18 and 28, 144
 // rows 44 and 31; of 500 keys, 384 rows 14 and 25.
-inline bool prefer_many(int64_t units, int64_t rows, int64_t keys, int D) {
+//
+// Of a 4-bit cache the few-rows kernel takes 0.1 D ns, the other converts what it
+// reads and takes what it did.  64 sequences of 1000 keys, 40 rows at D = 128 and 256:
+// 50 and 75, 101 and 121 us, 72 rows 69 and 75, 148 and 127, 144 rows 113 and 86, 249
+// and 147; one of 8000 keys, 40 rows 20 and 24, 25 and 33, 288 rows 44 and 42, 78 and 55.
+inline bool prefer_many(int64_t units, int64_t rows, int64_t keys, int D, bool four = false) {
   const double per_cu = static_cast<double>(units) / 256;
-  const double few = static_cast<double>((rows + 31) / 32) * per_cu * (keys + 130.0) * 0.19 * D;
+  const double few = static_cast<double>((rows + 31) / 32) * per_cu * (keys + 130.0) *
+                     (four ? 0.1 : 0.19) * D;
   const double many = static_cast<double>((rows + kTileRows - 1) / kTileRows) * per_cu * keys *
                           (20 + 0.16 * D) + 7000;
   return rows > 32 && many < few;
@@ -129,7 +135,7 @@ inline AttnPlan plan_window(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t
                           (int64_t{sinks} + tile - 1) / tile * tile;
     return window > 0 && reach < kv ? reach : kv;
   };
-  p.many = prefer_many(B * Hk, rows, walk(kTileRows), D);
+  p.many = prefer_many(B * Hk, rows, walk(kTileRows), D, four);
   p.tile_rows = p.many ? kTileRows : rows <= 16 ? 16 : 32;
   p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   if (p.row_tiles > most / (B * Hk)) p.row_tiles = most / (B * Hk);

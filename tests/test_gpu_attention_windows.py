@@ -384,3 +384,108 @@ def test_graphs_of_one_capture_stream_replayed_on_two(pq, dev):  # noqa: F811
         for i in range(2):
             assert torch.equal(outs[i], want[i]), f"graph {i}, turn {turn}"
         assert torch.equal(third, want[2])
+
+
+def stretched(s, tile_rows, max_q, max_kv, window=0, sinks=0):
+    """That such a call cuts the batch's work evenly among workgroups: its workspace is
+    two slots of a row tile for each and a note for every row tile."""
+    lib = s.pq.load_library()
+    fn = (lib.pq1_kv4_attention_workspace_bytes if isinstance(s, Pages4) else
+          lib.pq1_paged_attention_ex_workspace_bytes)
+    B, T, Hq = len(s.qs), s.q.shape[0], s.Hk * s.G
+    got = fn(B, T, Hq, s.Hk, s.D, max_q, max_kv, window, sinks)
+    notes = 8 * s.Hk * (T * s.G // tile_rows + B + 1)
+    return got in [2 * wgs * tile_rows * (4 * s.D + 8) + notes for wgs in (256, 512)]
+
+
+STRETCHES = [
+    # new tokens, keys, Hk, G, D, page, type, out
+    ([1, 1], [1500, 1], 1, 1, 128, 16, BF16, BF16),                  # fewer steps than workgroups
+    ([1] * 40, [1 + 37 * i for i in range(40)], 4, 6, 256, 64, BF16, BF16),
+    ([1] * 40, [1400 - 35 * i for i in range(40)], 4, 6, 128, 8, F16, F32),
+    ([1, 0, 1, 0, 0, 1], [900, 70, 0, 0, 3, 2000], 3, 2, 128, 32, F16, F16),
+    ([4, 1, 0, 6, 2], [700, 2, 5, 300, 1300], 2, 4, 256, 16, BF16, F32),
+    ([40, 3, 17], [900, 3, 650], 2, 5, 128, 16, BF16, BF16),         # more tokens than was said
+    ([1] * 130, [(i * 41) % 160 for i in range(130)], 1, 8, 256, 4, F16, F16),
+    ([2] * 3 + [0] * 70 + [3] * 3, [500] * 3 + [9] * 70 + [800] * 3, 2, 2, 128, 16, BF16, BF16),
+]
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("case", STRETCHES, ids=range(len(STRETCHES)))
+def test_work_cut_evenly(pq, dev, case, kind):  # noqa: F811
+    """Batches whose work is cut into stretches, whatever tiles these begin and end in:
+    all keys, and first keys before a window that leaves none out or nearly all."""
+    qs, kvs, Hk, G, D, page, dt, dout = case
+    s = kind(pq, dev, qs, kvs, Hk, G, D, page, dt, seed=len(qs))
+    max_q = min(max(qs), 32 // G)
+    tile_rows = 16 if max_q * G <= 16 else 32
+    for window, sinks in ((0, 0), (10 ** 8, 7), (90, 10 ** 8)):
+        if window == 0 and kind is Pages:
+            continue                        # the plain kernel's
+        assert stretched(s, tile_rows, max_q, 2 ** 31, window, sinks), (window, sinks)
+        got = s.run(max_q=max_q, max_kv=2 ** 31, window=window, sinks=sinks, out_dtype=dout)
+        s.check(got, True, window, sinks, where=f"window {window}")
+        again = s.run(max_q=max_q, max_kv=2 ** 31, window=window, sinks=sinks, out_dtype=dout)
+        assert torch.equal(got, again), "the same call gives the same bits"
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_odd_values_in_work_cut_evenly(pq, dev, kind):  # noqa: F811
+    """Infinities and NaN in values that only the last of a sequence's rows sees, in tiles
+    that several workgroups have parts of."""
+    qs, kvs = [3, 1, 5, 2], [2000, 900, 1400, 40]
+    s = kind(pq, dev, qs, kvs, 2, 3, 128, 16, BF16, seed=4)
+    for b, n in enumerate(kvs):
+        s.v[b][n - 1, 0, 5] = float("nan")
+        s.v[b][n - 1, 1, 77] = float("-inf")
+    s.fill()
+    assert stretched(s, 16, 5, 2 ** 31, 10 ** 8, 4)
+    for out in (BF16, F32):
+        got = s.run(max_q=5, max_kv=2 ** 31, window=10 ** 8, sinks=4, out_dtype=out)
+        s.check(got, True, 10 ** 8, 4, where="odd values")
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_work_cut_evenly_in_graphs(pq, dev, kind):  # noqa: F811
+    """A captured call cuts by the lengths of its replay; two graphs and an eager call at
+    once, each with its own workspace."""
+    sizes = [([1, 1, 1], [700, 1500, 90]), ([2, 1, 4], [800, 20, 1100]), ([1, 1, 1], [64, 900, 300])]
+    batches = [kind(pq, dev, qs, kvs, 4, 6, 256, 64, BF16, seed=i) for i, (qs, kvs) in enumerate(sizes)]
+    args = [b.args() for b in batches]
+    kw = dict(max_q=4, max_kv=2 ** 31, window=10 ** 8, sinks=5)
+    call = lambda i: batches[i].call(*args[i], **kw)
+    assert all(stretched(b, 32, 4, 2 ** 31, 10 ** 8, 5) for b in batches)
+    want = [call(i).clone() for i in range(3)]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(i))
+        graphs.append(g)
+    for turn in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay()
+            third = call(2)
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], want[i]), f"graph {i}, turn {turn}"
+        assert torch.equal(third, want[2])
+    # other lengths in the same tensors
+    kv = args[0][4]
+    for lens in ([1, 1400, 33], [700, 3, 0], [640, 1500, 90]):
+        kv.copy_(torch.tensor(lens, dtype=torch.int32))
+        graphs[0].replay()
+        got = outs[0].clone()
+        assert torch.equal(got, call(0)), lens
+        for b, n in enumerate(lens):
+            e, w, spread = ref4.attention(batches[0].q[b:b + 1], batches[0].k[b][:n],
+                                          batches[0].v[b][:n], 1 / 16, True, 0, 0)
+            check(got[b:b + 1], e, ref.attention_bound(
+                e, w, spread, n, float(batches[0].v[b].double().abs().max()), 256, BF16, BF16),
+                f"lengths {lens}, sequence {b}")
