@@ -132,8 +132,12 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
   constexpr int COPIES = KT / (CROWS * kTileWaves);
   constexpr int NB = D / 32;                    // blocks of 32 dimensions
   constexpr int EB = KT / 32;                   // blocks of 32 keys
-  constexpr int AHEAD = D == 256 ? 3 : 4;       // fragments in flight from LDS
   constexpr bool SINKS = F != kTwoByte, FOUR = F == kFourBit;
+  // Fragments in flight from LDS.  (With three, what walks two runs of keys and takes
+  // its second product three times keeps a row of Q in memory, and the load of that
+  // waits for the copies too: prompts of 500 to 6000 tokens in a window of 1024,
+  // bf16, 739 us for 714.)
+  constexpr int AHEAD = D < 256 ? 4 : F == kTwoByteSinks && NP == 3 ? 2 : 3;
   constexpr int BUFFERS = FOUR ? 2 : 3;
   __shared__ __attribute__((aligned(TILE))) char k_lds[BUFFERS * TILE], v_lds[BUFFERS * TILE];
   __shared__ int32_t page_lds[kPages + (SINKS ? 4 : 1)];

@@ -5,12 +5,14 @@ import math
 
 import pytest
 import torch
+from hypothesis import given, settings, strategies as st
 
 import kv4_reference as ref4
 from conftest import gpu_available
 from gemm_hadamard_rotated_amd import pq1
-from test_attention_abi_cpu import (ALIAS, ALIGN, ARG, BF16, BIG, F16, F32, GEMM, GIB, NULL, OK, P,
-                                    SHAPE, cache, heads, lib, spec)  # noqa: F401 (lib: a fixture)
+from test_attention_abi_cpu import (ALIAS, ALIGN, ARG, BF16, BIG, CODES, F16, F32, GEMM, GIB, NULL,
+                                    OK, P, SETTINGS, SHAPE, cache, cache_any, heads, lib, opt,  # noqa: F401
+                                    ptr, size, small, spec, spec_any, view)
 
 needs_no_gpu = pytest.mark.skipif(gpu_available(), reason="needs a host without a visible GPU")
 DEVICE = 6
@@ -261,3 +263,67 @@ def test_reference_gradient_by_autograd():
 
 def test_struct_sizes():
     assert ctypes.sizeof(pq1.Pq1Kv4Cache) == 56 and ctypes.sizeof(pq1.Pq1HeadNorm) == 24
+
+
+# Any arguments at all: a code that the header names, and no crash.
+weights_any = st.builds(pq1.Pq1HeadNorm, ptr, ptr, st.floats(width=32))
+cache4_any = st.builds(pq1.Pq1Kv4Cache, ptr, ptr, ptr, ptr, st.integers(-1, 4), small, size, small, small)
+
+
+@needs_no_gpu
+@settings(**SETTINGS)
+@given(x=opt(view), y=opt(view), w=ptr, eps=st.floats(width=32), p=ptr, f=ptr, s=opt(spec_any), T=size,
+       H=small, D=small)
+def test_norm_any_arguments(lib, x, y, w, eps, p, f, s, T, H, D):  # noqa: F811
+    assert lib.pq1_norm_rope(x, y, w, eps, p, f, s, T, H, D, None) in CODES
+
+
+@needs_no_gpu
+@settings(**SETTINGS)
+@given(g=opt(view), x=opt(view), d=opt(view), w=ptr, dw=ptr, eps=st.floats(width=32), p=ptr, f=ptr,
+       s=opt(spec_any), T=size, H=small, D=small, ws=ptr, n=st.sampled_from([0, 1 << 20, 1 << 40]))
+def test_norm_grad_any_arguments(lib, g, x, d, w, dw, eps, p, f, s, T, H, D, ws, n):  # noqa: F811
+    assert lib.pq1_norm_rope_grad(g, x, d, w, dw, eps, p, f, s, T, H, D, ws, n, None) in CODES
+    assert lib.pq1_norm_rope_grad_workspace_bytes(T, D) >= 0
+
+
+@needs_no_gpu
+@settings(**SETTINGS)
+@given(k=opt(view), v=opt(view), sl=ptr, q=opt(view), qo=opt(view), Hq=small, p=ptr, f=ptr,
+       s=opt(spec_any), n=opt(weights_any), c=opt(cache_any), c4=opt(cache4_any), T=size)
+def test_appends_any_arguments(lib, k, v, sl, q, qo, Hq, p, f, s, n, c, c4, T):  # noqa: F811
+    assert lib.pq1_kv_append_ex(k, v, sl, q, qo, Hq, p, f, s, n, c, T, None) in CODES
+    assert lib.pq1_kv4_append(k, v, sl, q, qo, Hq, p, f, s, n, c4, T, None) in CODES
+    assert lib.pq1_kv4_read(c4, sl, k, v, T, None) in CODES
+
+
+@needs_no_gpu
+@settings(**SETTINGS)
+@given(q=opt(view), o=opt(view), c=opt(cache_any), c4=opt(cache4_any), t=ptr, mp=size, cu=ptr, kv=ptr,
+       B=size, T=size, Hq=small, mq=size, mkv=size, sc=st.floats(width=32), ca=st.integers(-1, 2), w=small,
+       si=small, ws=ptr, n=st.sampled_from([0, 1 << 20, 1 << 40]))
+def test_attention_any_arguments(lib, q, o, c, c4, t, mp, cu, kv, B, T, Hq, mq, mkv, sc, ca, w,  # noqa: F811
+                                 si, ws, n):
+    for fn, of in ((lib.pq1_paged_attention_ex, c), (lib.pq1_kv4_attention, c4)):
+        assert fn(q, o, of, t, mp, cu, kv, B, T, Hq, mq, mkv, sc, ca, w, si, ws, n, None) in CODES
+        H, D = (of.heads, of.dim) if of is not None else (4, 64)
+        assert lib.pq1_paged_attention_ex_workspace_bytes(B, T, Hq, H, D, mq, mkv, w, si) >= 0
+        assert lib.pq1_kv4_attention_workspace_bytes(B, T, Hq, H, D, mq, mkv, w, si) >= 0
+
+
+@needs_no_gpu
+@settings(**SETTINGS)
+@given(B=st.integers(1, 1 << 23), T=st.integers(1, 1 << 30), Hk=st.integers(1, 1024),
+       G=st.integers(1, 64), D=st.sampled_from([64, 128, 256]), mq=st.integers(0, 1 << 62),
+       mkv=st.integers(0, 1 << 62), w=st.integers(0, (1 << 31) - 1), si=st.integers(0, (1 << 31) - 1))
+def test_attention_plans_of_any_size(lib, B, T, Hk, G, D, mq, mkv, w, si):  # noqa: F811
+    """Sizes alone: a plan is refused, or the workspace it asked for does."""
+    si = si if w else 0
+    views = (heads(1 << 52, n=Hk * G, D=D, hs=D), heads(1 << 53, n=Hk * G, D=D, hs=D))
+    rest = (P(1 << 54), 9, P(1 << 55), P(1 << 56), B, T, Hk * G, mq, mkv, 0.1, 1, w, si, P(1 << 57))
+    four = pq1.Pq1Kv4Cache(1 << 50, 1 << 48, 1 << 51, 1 << 49, BF16, 16, 9, Hk, D)
+    need = lib.pq1_kv4_attention_workspace_bytes(B, T, Hk * G, Hk, D, mq, mkv, w, si)
+    assert lib.pq1_kv4_attention(*views, four, *rest, need, None) in (SHAPE, DEVICE)
+    need = lib.pq1_paged_attention_ex_workspace_bytes(B, T, Hk * G, Hk, D, mq, mkv, w, si)
+    two = cache(n=Hk, D=D, k=1 << 50, v=1 << 51)
+    assert lib.pq1_paged_attention_ex(*views, two, *rest, need, None) in (SHAPE, DEVICE)
