@@ -83,7 +83,10 @@ __device__ __forceinline__ TileAt find_tile(const AttnArgs& a, const int32_t* ta
 // Four-bit caches (F = kFourBit) go the same way.  A lane's 16 bytes of a K row are
 // the 32 codes of one scale: they make four operands, for which the queries are
 // read in the same order.  Of V a lane reads D / 16 codes of each of its 8 keys.
-// Both become pairs of T by one instruction for two codes.
+// Both become pairs of T by one instruction for two codes, each used once.  64 tokens at
+// 200 to 8000 keys, 4 heads, D = 256: 66 us and 5 to join, 4.5 TB/s of the codes and
+// scales, vector instructions 42 % of the time and matrix ones 13; one token at 131070
+// keys 42 us.  Queries kept in LDS and V a tile ahead were slower (80 -> 91 us).
 //
 // This is one workgroup's part: rows r0 .. of a tile, places [k0, k1) of its walk.
 template <typename T, typename TO, int D, int RB, bool RUNS, CacheForm F, typename Out>

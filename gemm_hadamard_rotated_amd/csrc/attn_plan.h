@@ -1,5 +1,6 @@
 // How an attention call is cut into workgroups.  Host code without a GPU in it:
-// a function of the call's sizes alone.
+// a function of the call's sizes alone (where it says stretches, the kernel cuts
+// these by the sequences' lengths).
 #pragma once
 
 #include <stddef.h>

@@ -600,7 +600,9 @@ pq1_status pq1_kv4_read(const pq1_kv4_cache* cache, const int64_t* slots, const 
  *   sinks      >= 0; above 0 only with window > 0 (PQ1_ERR_ARG).
  *   workspace  pq1_paged_attention_ex_workspace_bytes(...) bytes, as there; it
  *              depends on window and sinks.
- * Everything else as pq1_paged_attention. */
+ * Results do not depend on scheduling: keys are cut by the call's sizes and the
+ * sequences' lengths, and the parts are joined in order (so a row's last bits may
+ * differ with what else is in the batch).  Everything else as pq1_paged_attention. */
 pq1_status pq1_paged_attention_ex(const pq1_heads* q, const pq1_heads* out,
                                   const pq1_kv_cache* cache, const int32_t* page_table,
                                   int64_t max_pages, const int32_t* cu_q, const int32_t* kv_len,
