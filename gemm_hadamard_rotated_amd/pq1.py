@@ -914,12 +914,16 @@ class HeadNorm:
             if w.shape != given[0].shape or w.dim() != 1:
                 raise ValueError(f"weights must be 1-D, [dim], got {[tuple(w.shape) for w in given]}")
         _need_eps(eps, "HeadNorm")
-        self._k_weight, self._q_weight, self.eps = k_weight, q_weight, float(eps)
+        self._k_weight, self._q_weight, self._eps = k_weight, q_weight, float(eps)
         self._device, self._dim = given[0].device, given[0].numel()
-        self._struct = Pq1HeadNorm(_ptr(q_weight), _ptr(k_weight), self.eps)
+        self._struct = Pq1HeadNorm(_ptr(q_weight), _ptr(k_weight), self._eps)
 
-    # The tensors given; their addresses went into the struct, so other ones
-    # need another HeadNorm.
+    # What was given; it went into the struct, the tensors as addresses, so other
+    # ones need another HeadNorm.
+    @property
+    def eps(self) -> float:
+        return self._eps
+
     @property
     def k_weight(self) -> Optional[torch.Tensor]:
         return self._k_weight

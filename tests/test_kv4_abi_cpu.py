@@ -231,6 +231,12 @@ def test_tensors_whose_address_is_kept_cannot_be_exchanged(cls, name):
         setattr(object.__new__(cls), name, torch.zeros(4))
 
 
+def test_eps_of_a_norm_cannot_be_changed():
+    """It went into the struct that the calls pass on."""
+    with pytest.raises(AttributeError):
+        object.__new__(pq1.HeadNorm).eps = 1e-3
+
+
 # ---------------------------------------------------------------------------
 # The 64-bit forms that the GPU tests rest on
 # ---------------------------------------------------------------------------
