@@ -7,7 +7,10 @@ A layer's step is four calls after the rotation of its input: the stacked
 query/key/value projection, pq1_kv_append (queries and keys rotated by their
 positions on the way), pq1_paged_attention, and the output projection with its
 own rotation.  Chunks of a prompt use the bf16 GEMM, single tokens the fused
-decode step; the attention calls are the same for both.
+decode step; the attention calls are the same for both.  With norms=True queries
+and keys are normed on the way into the cache, with bits=4 that holds 4-bit numbers
+(pq1_kv4_append, pq1_kv4_attention), and with a window each token sees the last
+`window` ones and the first `sinks`.
 """
 import os
 import sys
@@ -23,15 +26,24 @@ class AttentionLayer:
     """Random 1-bit weights of the tested 27B model's head shapes."""
 
     def __init__(self, hidden=5120, heads=24, kv_heads=4, dim=256, rot=64, sections=(11, 11, 10),
-                 pages=64, page_size=64, seed=0, device="cuda:0"):
+                 pages=64, page_size=64, seed=0, device="cuda:0", norms=False, bits=16, window=0,
+                 sinks=0):
         self.hidden, self.heads, self.kv_heads, self.dim = hidden, heads, kv_heads, dim
+        self.window, self.sinks = window, sinks
         self.dev = torch.device(device)
         g = torch.Generator(device=self.dev).manual_seed(seed)
         self.qkv = self._weights((heads + 2 * kv_heads) * dim, hidden, g)
         self.out = self._weights(hidden, heads * dim, g)
         self.rope = pq1.Rope(rot, sections, freqs=pq1.rope_frequencies(rot, 1.0e6, self.dev),
                              interleaved=True)
-        self.cache = pq1.KVCache.empty(pages, page_size, kv_heads, dim, device=self.dev)
+        kind = pq1.KV4Cache if bits == 4 else pq1.KVCache
+        self.cache = kind.empty(pages, page_size, kv_heads, dim, device=self.dev)
+        self.append = pq1.pq1_kv4_append if bits == 4 else pq1.pq1_kv_append
+        self.attend = pq1.pq1_kv4_attention if bits == 4 else pq1.pq1_paged_attention
+        self.norm = None
+        if norms:
+            w = 1 + 0.1 * torch.randn(2, dim, device=self.dev, generator=g)
+            self.norm = pq1.HeadNorm(w[0], w[1])
 
     def _weights(self, N, K, g):
         bits = torch.randint(-2 ** 31, 2 ** 31, (N, K // 32), device=self.dev, generator=g).to(
@@ -54,9 +66,10 @@ class AttentionLayer:
         qkv = self._project(x, self.qkv)
         q, k, v = (qkv[:, a * D:b * D].unflatten(1, (b - a, D))
                    for a, b in ((0, H), (H, H + Hk), (H + Hk, H + 2 * Hk)))
-        q = pq1.pq1_kv_append(self.cache, k, v, slots, positions=positions, rope=self.rope, q=q)
-        o = pq1.pq1_paged_attention(q, self.cache, table, cu_q, kv_len, max_q, max_kv,
-                                    out_dtype=torch.float32)
+        q = self.append(self.cache, k, v, slots, positions=positions, rope=self.rope, q=q,
+                        norm=self.norm)
+        o = self.attend(q, self.cache, table, cu_q, kv_len, max_q, max_kv, window=self.window,
+                        out_dtype=torch.float32, sinks=self.sinks)
         return self._project(o.view(x.shape[0], H * D), self.out)
 
 
@@ -109,6 +122,11 @@ def main():
             layer(x[:n].contiguous(), **a)
         torch.cuda.synchronize()
         print(f"{label}: {(time.perf_counter() - t) / times * 1e6:.0f} us a layer")
+    layer = AttentionLayer(norms=True, bits=4, window=256, sinks=4)
+    run(layer, x, range(0, 16), [T])
+    parts = run(layer, x, range(40, 24, -1), [512, 300, 180] + [1] * 8)
+    print(f"normed, 4-bit cache, window of 256 and 4 first tokens: {list(parts.shape)}, "
+          f"finite {bool(torch.isfinite(parts).all())}")
     return float(error)
 
 

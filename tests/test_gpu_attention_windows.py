@@ -489,3 +489,35 @@ def test_work_cut_evenly_in_graphs(pq, dev, kind):  # noqa: F811
             check(got[b:b + 1], e, ref.attention_bound(
                 e, w, spread, n, float(batches[0].v[b].double().abs().max()), 256, BF16, BF16),
                 f"lengths {lens}, sequence {b}")
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_attention_layer_example(pq, dev, bits):  # noqa: F811
+    """The example's layer with norms and a window with first keys: in chunks and single
+    tokens it runs, and its attention is the formula's over what its cache holds."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                                    "examples"))
+    import attention_layer as ex
+    layer = ex.AttentionLayer(hidden=1024, heads=4, kv_heads=2, dim=256, pages=40, page_size=16,
+                              norms=True, bits=bits, window=40, sinks=3)
+    x = torch.randn(150, 1024, device=dev, generator=torch.Generator(device=dev).manual_seed(1))
+    parts = ex.run(layer, x, range(30, 20, -1), [64, 1, 50, 33, 1, 1])
+    assert parts.shape == x.shape and bool(torch.isfinite(parts).all())
+    whole = ex.run(layer, x, range(10), [150])
+    D, a = 256, ex.Sequence(layer, range(10)).extend(150)
+    qkv = layer._project(x, layer.qkv)
+    q, k, v = (qkv[:, i * D:j * D].unflatten(1, (j - i, D)) for i, j in ((0, 4), (4, 6), (6, 8)))
+    qr = layer.append(layer.cache, k, v, a["slots"], positions=a["positions"], rope=layer.rope, q=q,
+                      norm=layer.norm)
+    o = layer.attend(qr, layer.cache, a["table"], a["cu_q"], a["kv_len"], 150, 150, window=40, sinks=3,
+                     out_dtype=F32)
+    assert torch.equal(layer._project(o.view(150, 4 * D), layer.out), whole)
+    if bits == 4:
+        kc, vc = pq.pq1_kv4_read(layer.cache, a["slots"])
+    else:
+        kc, vc = (t[:10].transpose(1, 2).reshape(160, 2, D)[:150] for t in (layer.cache.k, layer.cache.v))
+    e, w, spread = ref4.attention(qr.cpu(), kc.cpu(), vc.cpu(), D ** -0.5, True, 40, 3)
+    check(o, e, ref.attention_bound(e, w, spread, 150, float(vc.double().abs().max()), D, BF16, F32),
+          "example")
