@@ -489,3 +489,33 @@ def test_calls_in_graphs_and_on_streams(pq, dev):
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+def test_norm_past_32_bits(pq, dev):
+    """More than 2^31 elements: the last tokens as in a call of their own, and the
+    weight's gradient as that of two halves together."""
+    T, H, D = 530000, 16, 256
+    g = torch.Generator(device=dev).manual_seed(2)
+    x = torch.randn(T, H, D, device=dev, dtype=BF16, generator=g)
+    w = (1 + drawn((D,), 6, F32, 0.3)).to(dev)
+    rope, _ = rotation(pq, dev, 64, (32,), "halves", False)
+    pos = torch.arange(T, dtype=torch.int32, device=dev).flip(0)[None].contiguous()
+    y = pq.pq1_norm_rope(x, w, pos, rope)
+    for at in (0, T // 2 + 1, T - 7):
+        few = slice(at, at + 7)
+        assert torch.equal(y[few], pq.pq1_norm_rope(x[few].clone(), w, pos[:, few].contiguous(), rope))
+    dx, _ = pq.pq1_norm_rope_grad(y, x, w, pos, rope, weight_grad=False)
+    for at in (0, T - 7):
+        few = slice(at, at + 7)
+        assert torch.equal(dx[few], pq.pq1_norm_rope_grad(y[few].clone(), x[few].clone(), w,
+                                                          pos[:, few].contiguous(), rope,
+                                                          weight_grad=False)[0])
+    # a workgroup's lanes add up at most T H / 1024 heads in fp32, every eighth each
+    # and then their eight sums; what is added is off by a few 2^-24 of itself
+    half = T // 2
+    _, dw = pq.pq1_norm_rope_grad(y, x, w, dx=dx)
+    parts = [pq.pq1_norm_rope_grad(y[c], x[c], w, dx=dx[c])[1].double()
+             for c in (slice(0, half), slice(half, T))]
+    _, size = pq.pq1_norm_rope_grad(y.abs_(), x.abs_(), w, dx=dx)
+    bound = 2 * (T * H / 1024 / 8 + 8 + 8) * 2.0 ** -24 * size.double()
+    assert bool(((dw.double() - parts[0] - parts[1]).abs() <= bound).all())
