@@ -550,22 +550,53 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
         const float inv = 1.0f / sum;
         int lo, hi;
         visible(a, s, i, &lo, &hi);
+        TO* const out = static_cast<TO*>(a.out) + (s.q0 + i) * a.o_ts + hq * a.o_hs;
+        auto value = [&](int n, int e) { return hi > lo ? o[n][e] * inv : 0.0f; };
+        bool done = false;
+        if constexpr (sizeof(TO) == 2) {
+          // Two eights of a row at a time: each half of the wave has four of either,
+          // and takes one of them whole (stores of four: 433 us for 412 in prompts of
+          // 500 to 6000 tokens in a window of 1024, 388 for 378 in those of 30 to 4000).
+          done = tg.nsplit == 1;
+          if (done) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const int d = 32 * n + 8 * i4 + 4 * g;
-            float y[4];
+              for (int i4 = 0; i4 < 4; i4 += 2) {
+                U4 y;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = o[n][4 * i4 + c];
-            if (tg.nsplit > 1) {
-              store_wide(part_o + at_row * D + d, y);
-            } else {
+                for (int w = 0; w < 2; ++w) {
+                  Pack<TO, 2> x[2];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) y[c] = hi > lo ? y[c] * inv : 0.0f;
-              store_wide(static_cast<TO*>(a.out) + (s.q0 + i) * a.o_ts + hq * a.o_hs + d, y);
-            }
+                  for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                      x[e].e[c] = static_cast<TO>(value(n, 4 * (i4 + e) + 2 * w + c));
+                  const auto z = __builtin_amdgcn_permlane32_swap(
+                      __builtin_bit_cast(uint32_t, x[0]), __builtin_bit_cast(uint32_t, x[1]), false,
+                      false);
+                  y[w] = z[0];
+                  y[2 + w] = z[1];
+                }
+                *reinterpret_cast<U4*>(out + 32 * n + 8 * (i4 + g)) = y;
+              }
           }
+        }
+        if (!done) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              const int d = 32 * n + 8 * i4 + 4 * g;
+              float y[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) y[c] = tg.nsplit > 1 ? o[n][4 * i4 + c] : value(n, 4 * i4 + c);
+              if (tg.nsplit > 1)
+                store_wide(part_o + at_row * D + d, y);
+              else
+                store_wide(out + d, y);
+            }
+        }
       }
     }
 
