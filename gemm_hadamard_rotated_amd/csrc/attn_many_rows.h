@@ -14,12 +14,12 @@
 // and a row's maximum and sum need one exchange between the halves of a wave.
 //
 // Bound: the matrix instructions and, for small D, the softmax between them.
-// 8192 rows of 8 cache heads against 7168 keys take 445 to 454 us at D = 256
-// (1061 to 1082 TFLOP/s), 255 to 261 us at 128 (921 to 945) and 186 to 188 us at
-// 64 (641 to 646); a large library product reaches 1263 TFLOP/s on the same card.
-// An fp32 result takes the second product three times for bf16 caches, 769 to
-// 792, 429 to 440 and 318 to 324 us, and twice for f16, 658 to 681, 362 to 376
-// and 238 to 241 us.
+// 8192 rows of 8 cache heads against 7168 keys take 435 to 459 us at D = 256
+// (1048 to 1106 TFLOP/s), 240 to 254 us at 128 (946 to 1001) and 160 to 165 us at
+// 64 (728 to 753); a large library product reaches 1263 TFLOP/s on the same card.
+// An fp32 result takes the second product three times for bf16 caches, 770, 426
+// to 440 and 304 to 324 us, and twice for f16, 658 to 681, 362 to 376 and 234 to
+// 241 us.
 // What was measured on the way (D = 128 of the above unless said): 64 rows a
 // wave, one wave a SIMD: slower (759 against 505 us for 2048 tokens after 6144
 // at D = 256); page numbers from LDS and no load waited for in the loop, so
@@ -617,8 +617,8 @@ hipError_t launch_tiles(const AttnPlan& plan, const Args<F>& a, void* workspace,
   float2* part_ml =
       reinterpret_cast<float2*>(part_o + static_cast<int64_t>(plan.nsplit) * a.T * a.Hk * a.G * D);
   const dim3 grid(static_cast<uint32_t>(a.B * a.Hk * plan.row_tiles * plan.nsplit));
-  // 32-bit offsets into K and V where they reach (D = 64 of the above: 193 us
-  // with 64-bit ones, 186 with these)
+  // 32-bit offsets into K and V where they reach (D = 64 of the above: 7 us less
+  // than with 64-bit ones)
   const uint64_t cache_rows = static_cast<uint64_t>(a.pages) * a.Hk << a.page_shift;
   const bool wide = (cache_rows * (F == kFourBit ? D / 2 : 2 * D)) >> 32 != 0;
   if (wide)

@@ -2,7 +2,7 @@
 // (attn_many_rows.h).
 //
 // Prompts of 500 to 6000 tokens in a window of 1024 with 16 first keys, 6 query heads to
-// each of 4 cache heads, D = 256: 412 us, 809 TFLOP/s of what rows see.  A tile of 43
+// each of 4 cache heads, D = 256: 403 to 412 us, 809 to 827 TFLOP/s of what rows see.  A tile of 43
 // tokens walks over 34 key tiles, of which 6 are edges (masks 1 % of the time, taking
 // invisible values out of V 4 %); the rest of what keeps it from the 990 of long chunks
 // is a workgroup's beginning and end, which nothing overlaps with one workgroup to a CU,
