@@ -534,9 +534,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void few_rows_kernel
 // Stretches, for batches whose lengths may differ: all tiles' steps, one tile after
 // another (after kStart steps for each one's beginning, which costs as much), are a
 // line, and each of as many workgroups as the device holds takes a stretch of the
-// same length (64 tokens at 200 to 8000 keys, 4-bit, D = 256: 113 us with one
-// workgroup for each, 83 in eight parts, 79 with kStart 0, 72 with 2; all at 4000
-// keys: 64, 70, 62 and 63 us).  Every workgroup finds its stretch by itself, from
+// same length (64 tokens at 200 to 8000 keys, 4-bit, D = 256: 93 us with one
+// workgroup for each, 83 in eight parts, 81 with kStart 0, 72 with 2; all at 4000
+// keys: 55, 71, 62 and 64 us).  Every workgroup finds its stretch by itself, from
 // the sequences' lengths.  Only the first and the last piece of a stretch can be
 // parts of a tile's keys; they go to the stretch's two slots, and the workgroup
 // with a tile's first piece notes for the join who has the others.
