@@ -320,12 +320,11 @@ __device__ __forceinline__ void few_rows_part(const Args<F>& a, const Seq& s, co
                                     ? 0xffffffffu
                                     : 0u;
           if constexpr (FOUR) {
-            // codes of zero under a scale that is a number
-            const bool take = seen != 0 && (one_token || vs[e] <= kMostExp<T> + 127);
-            odd |= seen != 0 && !take ? kOdd : 0u;
-            vs[e] = take ? vs[e] : 127u;
+            // codes of zero, under a scale that is a number
 #pragma unroll
-            for (int w = 0; w < VW; ++w) vr[e][w][0] = take ? vr[e][w][0] : 0u;
+            for (int w = 0; w < VW; ++w) vr[e][w][0] &= seen;
+            vs[e] = seen != 0 ? vs[e] : 127u;
+            odd |= vs[e] > kMostExp<T> + 127 ? kOdd : 0u;
             continue;
           }
 #pragma unroll
@@ -339,11 +338,20 @@ __device__ __forceinline__ void few_rows_part(const Args<F>& a, const Seq& s, co
         if (!one_token && __any((odd & kOdd) != 0)) {
           odd_values = true;
 #pragma unroll
-          for (int e = 0; e < (FOUR ? 0 : 8); ++e)
+          for (int e = 0; e < 8; ++e) {
+            if constexpr (FOUR) {
+              const bool far = vs[e] > kMostExp<T> + 127;
+#pragma unroll
+              for (int w = 0; w < VW; ++w)
+                vr[e][w][0] &= far ? ~odd_codes<T>(vr[e][w][0], vs[e]) : 0xffffffffu;
+              vs[e] = vs[e] != kNanScale ? vs[e] : 127u;
+              continue;
+            }
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
               for (int w = 0; w < DV / 2; ++w) vr[e][c][w] = finite_or_zero<T>(vr[e][c][w]);
+          }
         }
       }
       const uint32_t gone = at.gone >> 4 * g;

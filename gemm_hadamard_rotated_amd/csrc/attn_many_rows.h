@@ -296,11 +296,18 @@ __global__ __launch_bounds__(64 * kTileWaves) void many_rows_kernel(Args<F> a, T
       if (is_edge<F>(a, pt, j0, KT, gone != 0)) {
         const int j = j0 + r;
         const bool seen = (j >= pt.lo || j < sinks_of<F>(a)) && j < pt.hi && !(gone >> r & 1);
-        const bool take = seen && vscale <= kMostExp<T> + 127;
-        odd4 |= seen && !take;
-        vscale = take ? vscale : 127u;
 #pragma unroll
-        for (int n = 0; n < WORDS; ++n) vc[n] = take ? vc[n] : 0u;
+        for (int n = 0; n < WORDS; ++n) vc[n] = seen ? vc[n] : 0u;
+        vscale = seen ? vscale : 127u;
+        if (vscale > kMostExp<T> + 127) {
+#pragma unroll
+          for (int n = 0; n < WORDS; ++n) {
+            const uint32_t out = odd_codes<T>(vc[n], vscale);
+            odd4 |= out != 0;
+            vc[n] &= ~out;
+          }
+          vscale = vscale != kNanScale ? vscale : 127u;
+        }
       }
 #pragma unroll
       for (int n = 0; n < WORDS; ++n) {

@@ -282,8 +282,8 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t pair) {
 }
 
 // Element d of a row of V.  `row` counts elements of T from the cache's start, also
-// where the cache holds 4-bit ones: then what was not taken out of a tile, a group
-// of finite values, counts as zero.
+// where the cache holds 4-bit ones.  There a group under a scale of the append's
+// range, which has no infinity, counts as zero.
 template <typename T, CacheForm F>
 __device__ __forceinline__ float value_at(const Args<F>& a, const T* row, int d) {
   if constexpr (F == kFourBit) {

@@ -50,6 +50,18 @@ __device__ __forceinline__ void pairs_of(uint32_t codes, float scale, uint32_t (
   out[3] = pair_of<T, 3>(codes, scale);
 }
 
+// The codes of a word, all four bits of each, whose values under this scale are
+// infinities of T (from `least` on: 4 at twice the largest scale of the append, then
+// 2, 1 and 0.5) or NaN (all of them).  The scale is past the append's range.
+template <typename T>
+__device__ __forceinline__ uint32_t odd_codes(uint32_t codes, uint32_t byte) {
+  const int past = static_cast<int>(byte) - (kMostExp<T> + 127);
+  const int least = byte == kNanScale ? 0 : past > 3 ? 1 : 8 - 2 * past;
+  const uint32_t top =
+      ((codes & 0x77777777u) + static_cast<uint32_t>(8 - least) * 0x11111111u) & 0x88888888u;
+  return top | (top - (top >> 3));
+}
+
 // Scale byte of a group whose largest magnitude has these bits: the least
 // exponent e with top <= 7 * 2^e, so that the largest code, 6, is off by no more
 // than half the step below it.

@@ -590,8 +590,8 @@ pq1_status pq1_kv4_append(const pq1_heads* k, const pq1_heads* v, const int64_t*
 /* Rows of a 4-bit cache as numbers: token t of k_out and v_out ([T][heads][dim]
  * views of one type, any of the three; either may be NULL) is row slots[t] of
  * every head.  Slots may repeat; one outside the cache gives zeros.  Values are
- * exact (scales outside the append's range may round, or give infinities, in
- * two-byte types). */
+ * exact (scales outside the append's range may round in two-byte types, and give
+ * infinities where a value is past the type's largest). */
 pq1_status pq1_kv4_read(const pq1_kv4_cache* cache, const int64_t* slots, const pq1_heads* k_out,
                         const pq1_heads* v_out, int64_t T, void* stream);
 
@@ -615,8 +615,9 @@ size_t pq1_paged_attention_ex_workspace_bytes(int64_t B, int64_t T, int32_t Hq, 
 
 /* The same over a 4-bit cache: what pq1_paged_attention_ex gives for a cache that
  * holds the values of pq1_kv4_read, up to the order of sums.  q is of the cache's
- * dtype, out of that type or fp32.  A group whose scale is 255 gives NaN in the rows
- * that see it and no others; so may scales past the append's range. */
+ * dtype, out of that type or fp32.  A group whose scale is 255 is NaN, and codes under
+ * scales past the append's range that stand for no finite number of that type are
+ * infinities: both reach the rows that see them and no others. */
 pq1_status pq1_kv4_attention(const pq1_heads* q, const pq1_heads* out, const pq1_kv4_cache* cache,
                              const int32_t* page_table, int64_t max_pages, const int32_t* cu_q,
                              const int32_t* kv_len, int64_t B, int64_t T, int32_t Hq,
