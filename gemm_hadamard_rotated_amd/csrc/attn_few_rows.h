@@ -321,10 +321,11 @@ __device__ __forceinline__ void few_rows_part(const Args<F>& a, const Seq& s, co
                                     : 0u;
           if constexpr (FOUR) {
             // codes of zero, under a scale that is a number
+            const bool take = seen != 0 && (one_token || vs[e] != kNanScale);
+            odd |= seen != 0 && vs[e] > kMostExp<T> + 127 ? kOdd : 0u;
+            vs[e] = take ? vs[e] : 127u;
 #pragma unroll
-            for (int w = 0; w < VW; ++w) vr[e][w][0] &= seen;
-            vs[e] = seen != 0 ? vs[e] : 127u;
-            odd |= vs[e] > kMostExp<T> + 127 ? kOdd : 0u;
+            for (int w = 0; w < VW; ++w) vr[e][w][0] = take ? vr[e][w][0] : 0u;
             continue;
           }
 #pragma unroll
@@ -344,7 +345,6 @@ __device__ __forceinline__ void few_rows_part(const Args<F>& a, const Seq& s, co
 #pragma unroll
               for (int w = 0; w < VW; ++w)
                 vr[e][w][0] &= far ? ~odd_codes<T>(vr[e][w][0], vs[e]) : 0xffffffffu;
-              vs[e] = vs[e] != kNanScale ? vs[e] : 127u;
               continue;
             }
 #pragma unroll
