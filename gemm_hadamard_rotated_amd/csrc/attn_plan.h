@@ -151,13 +151,17 @@ inline AttnPlan plan_window(int64_t B, int64_t T, int Hq, int Hk, int D, int64_t
     return p;
   }
   // Few rows: whole tiles where keys are few, where a window keeps the lengths alike
-  // (48 sequences, window of 1024, 8 cache heads, D = 128, two-byte: 46 us, 54 in
-  // stretches) and where tiles are many; parts for one sequence or where they are
-  // short; else stretches, as many as the device holds at once.
+  // and where tiles are many; parts for one sequence or where they are short; else
+  // stretches, as many as the device holds at once.  A window does so up to about 0.6
+  // of the longest sequence (64 sequences of 200 to 8000 keys, 4 cache heads, D = 256,
+  // in stretches and whole: 4-bit, windows of 1024, 4000, 6000 and 8000 24 and 21, 59
+  // and 55, 69 and 76, 72 and 93 us; two-byte 63 and 52, 159 and 148, 193 and 194, 205
+  // and 234; 48 sequences of 8 heads, D = 128, two-byte 46 and 43, 120 and 122, 138 and
+  // 168, 146 and 188).
   const int per_cu = D == 256 && (!four || p.tile_rows == 32) ? 1 : 2;
   const int64_t slots = 256 * per_cu, steps = (keys + step - 1) / step;
   const int64_t n = (slots + units - 1) / units;
-  if (keys * D <= kShort || units >= (window > 0 ? 256 : 4 * slots)) return p;
+  if (keys * D <= kShort || units >= (5 * keys <= 3 * kv ? 256 : 4 * slots)) return p;
   p.joined = true;
   if (B == 1 || keys * D <= n * kPart) {
     p.nsplit = static_cast<int>(n < steps ? n : steps);

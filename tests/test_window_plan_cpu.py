@@ -107,6 +107,27 @@ def test_parts_cover_what_tiles_walk_over(plans):
                 assert walked(row0, tile_rows, G, n, kv, w, s, 32 if D == 256 else 64) <= nsplit * chunk, size
 
 
+def test_a_window_that_hides_no_key_is_cut_as_none(plans):
+    """And one that is short beside the longest sequence leaves the tiles of a large
+    batch whole."""
+    rng = random.Random(5)
+    sizes = [(64, 64, 24, 4, 256, 1, 8000, w, s, four) for w in (8000, 10 ** 6) for s in (0, 16)
+             for four in (0, 1)]
+    for _ in range(3000):
+        Hk, mkv = rng.choice([1, 2, 4, 8]), int(2 ** rng.uniform(0, 18))
+        B, n = rng.randint(1, 600), rng.choice([1, 1, 2, 6, 40])
+        sizes.append((B, B * n, Hk * rng.randint(1, 8), Hk, rng.choice([64, 128, 256]), n, mkv,
+                      mkv + rng.randint(0, 1000), rng.choice([0, 4, 100]), rng.randint(0, 1)))
+    none = [(*s[:7], 0, 0, s[9]) for s in sizes]
+    for size, got, want in zip(sizes, plans(sizes), plans(none)):
+        assert got == want, size
+    for four in (0, 1):
+        assert plans([(64, 64, 24, 4, 256, 1, 8000, 0, 0, four)])[0][7] > 0
+        whole = plans([(64, 64, 24, 4, 256, 1, 8000, 1024, 4, four),
+                       (48, 48, 32, 8, 128, 1, 30000, 1024, 4, four)])
+        assert all(p[4] == 1 and p[7] == 0 and not p[8] for p in whole)
+
+
 def test_notes_of_row_tiles_do_not_meet():
     """Where the kernels note a tile's pieces: q0 G / ROWS + b on, for sequences that
     follow one another; and never past the workspace, whatever cu_q holds."""
