@@ -80,9 +80,17 @@ __device__ __forceinline__ double just(double c) {
 // In fp64: the angle less the nearest multiple n of pi / 2 (taken as the sum of two
 // numbers; the first difference is exact but for its last rounding, for n up to
 // 2^31 the second's share is below 2^-24), then the power series up to x^17 and x^16,
-// whose rest is below 2^-58 for |x| <= pi / 4.
+// whose rest is below 2^-58 for |x| <= pi / 4.  From 2^48 on, where n itself begins to
+// be rounded and an angle is off by more than 2^-5, its whole turns go first, as above.
 __device__ __forceinline__ double2 turn_of(int32_t pos, double freq, bool inverse, double) {
-  const double angle = static_cast<double>(pos) * freq;
+  double angle = static_cast<double>(pos) * freq;
+  if (!(fabs(angle) < just(0x1p48))) {
+    // (the compiler may take the product into the difference, which then is its rounding,
+    // of any size)
+    double turn = static_cast<double>(pos) * (freq * just(0.15915494309189533577));
+    turn -= rint(turn);
+    angle = (turn - rint(turn)) * just(6.2831853071795864769);
+  }
   const double n = rint(angle * 0.63661977236758134);
   const double x = fma(-n, 6.123233995736766e-17, fma(-n, 1.5707963267948966, angle));
   const double z = x * x;
