@@ -565,12 +565,6 @@ struct Pieces {
   int count2;  // 2 count, plus 1 if the first piece begins its stretch
 };
 
-// Where stretches begin: about total w / wgs.  (In fp64, whose division is a tenth of
-// a 64-bit one's code, and the code of a workgroup's only pass is what a short call
-// waits for: any cut will do that all workgroups agree on and that leaves no stretch
-// empty, as the join counts on every one between two others.  With total / wgs at
-// least 1, and for 2^20 workgroups at most, the products are far enough from the
-// integers below them.)
 // The same in all lanes, as the compiler may know.
 __device__ __forceinline__ int64_t uniform(int64_t x) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
@@ -578,6 +572,12 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
   return static_cast<int64_t>(uint64_t{hi} << 32 | lo);
 }
 
+// Where stretches begin: about total w / wgs.  (In fp64, whose division is a tenth of
+// a 64-bit one's code, and the code of a workgroup's only pass is what a short call
+// waits for: any cut will do that all workgroups agree on and that leaves no stretch
+// empty, as the join counts on every one between two others.  With total / wgs at
+// least 1, and for 2^20 workgroups at most, the products are far enough from the
+// integers below them.)
 struct Cuts {
   int wgs;
   int64_t total;

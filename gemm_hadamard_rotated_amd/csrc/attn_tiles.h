@@ -51,8 +51,8 @@ __device__ __forceinline__ void visible(const AttnArgs& a, const Seq& s, int i, 
 //
 // In windows whose first `sinks` keys stay visible a tile walks over those and
 // then over the window: place w of its walk [start, end) is key w up to sink_end,
-// and key w + jump past it.  Both are multiples of 64, so that a tile of keys has
-// no jump inside.  Elsewhere places are keys.
+// and key w + jump past it.  Both are multiples of the walking kernel's key tile (KEYS
+// of split_keys), so that a tile of keys has no jump inside.  Elsewhere places are keys.
 struct Parts {
   int start;  // rounded down to a multiple of 32
   int end;
