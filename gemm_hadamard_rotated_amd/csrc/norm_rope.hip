@@ -19,7 +19,7 @@
 // Bound: memory; next to it the fp64 sums and, into a 4-bit cache, the codes (vector
 // instructions are 75 to 87 % of a busy CU's time).  8190 tokens of 24 heads of 256 in
 // bf16: 43.7 us, 4.6 TB/s (a large copy reaches 5.1), the gradient 68 us, 4.4 TB/s; 4001
-// tokens of 24 + 4 + 4 heads into a 4-bit cache 49 us; one token 3.3 us, where an empty
+// tokens of 24 + 4 + 4 heads into a 4-bit cache 51 us; one token 3.3 us, where an empty
 // kernel takes 3.  What paid: a workgroup walks over neighbouring heads with the next
 // one's loads in flight (a workgroup for each few heads: 57 and 97 us, and the append
 // 21 us more); two heads of a lane side by side took more registers and time (71 for 57
